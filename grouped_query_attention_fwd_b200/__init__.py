@@ -8,6 +8,12 @@ fallback: if the library is missing this module raises at import time.
     out = forward(q, k, v, mask=None, causal=False, scale=None)
     kv_append(cache_k, cache_v, k_new, v_new, kv_lens)
 
+and the same over a cache held in 4 bits (``q4.py``):
+
+    kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens)
+    k, v = kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=kv_lens)
+    out = forward_q4(q, cache_k, cache_v, kv_lens=kv_lens)
+
 q [B, Hq, Sq, D], k and v [B, Hkv, Sk, D] (CUDA tensors, bf16 or fp32, last
 dim contiguous), mask bool/uint8 [B, Sq, Sk] (True = attend, shared by all
 heads), ``scale`` defaults to 1/sqrt(D).  ``kv_lens`` (int32 CUDA [B]) makes
@@ -35,11 +41,12 @@ GQA_ERR_WORKSPACE, GQA_ERR_CUDA, GQA_ERR_TIMEOUT, GQA_ERR_ARG, GQA_ERR_DEVICE = 
 GQA_ERR_SCRATCH_LIMIT, GQA_ERR_KV_LENGTH, GQA_ERR_PAGE = 10, 11, 12
 STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 GQA_DTYPE_BF16, GQA_DTYPE_F32, GQA_DTYPE_F16 = 0, 1, 2
-KERNEL_NAMES = {0: "none", 1: "decode", 2: "prefill", 3: "f32", 4: "zero", 5: "nan"}
+KERNEL_NAMES = {0: "none", 1: "decode", 2: "prefill", 3: "f32", 4: "zero", 5: "nan", 6: "q4"}
 
 EXPORTS = ("gqa_query", "gqa_forward", "gqa_device_status", "gqa_status_string", "gqa_version",
            "gqa_forward_decode_noalloc", "gqa_kv_append", "gqa_debug_decode_trace",
-           "gqa_debug_decode_withhold")
+           "gqa_debug_decode_withhold", "gqa_q4_record_bytes", "gqa_kv_append_q4",
+           "gqa_kv_read_q4", "gqa_query_q4", "gqa_forward_q4")
 
 
 class Problem(ctypes.Structure):
@@ -172,6 +179,7 @@ def _torch():
 
 
 _workspaces = {}
+_replaced_workspaces = []  # outgrown ones: a captured graph may still point at one
 
 
 def _dtype_code(t) -> int:
@@ -293,8 +301,10 @@ def workspace_for(device, nbytes: int, stream=None):
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         with torch.cuda.device(idx), torch.cuda.stream(st):
-            ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
-        _workspaces[key] = ws
+            new = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
+        if ws is not None:
+            _replaced_workspaces.append(ws)
+        _workspaces[key] = ws = new
     return ws
 
 
@@ -425,3 +435,7 @@ def debug_decode_withhold(unit: int, wait_limit_ns: int) -> None:
     rc = _lib.gqa_debug_decode_withhold(int(unit), int(wait_limit_ns))
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_debug_decode_withhold")
+
+
+from .q4 import (Q4RowsDesc, forward_q4, kv_append_q4, kv_read_q4, q4_problem_for,  # noqa: E402,F401
+                 q4_record_bytes, query_q4)

@@ -22,7 +22,9 @@ bool half_paths(const gqa_problem& p) {
   return p.dtype == GQA_DTYPE_BF16 || p.dtype == GQA_DTYPE_F16;
 }
 
-int validate(const gqa_problem* pp) {
+}  // namespace
+
+int validate_problem(const gqa_problem* pp) {
   if (pp == nullptr) return GQA_ERR_NULL;
   const gqa_problem& p = *pp;
   if (p.dtype != GQA_DTYPE_BF16 && p.dtype != GQA_DTYPE_F32 && p.dtype != GQA_DTYPE_F16)
@@ -91,6 +93,8 @@ bool nothing_visible(const gqa_problem& p) {
   return false;
 }
 
+namespace {
+
 int pick_kernel(const gqa_problem& p) {
   if (p.batch == 0 || p.seq_q == 0) return GQA_KERNEL_NONE;
   if (p.seq_k == 0) return GQA_KERNEL_ZERO;
@@ -103,6 +107,8 @@ int pick_kernel(const gqa_problem& p) {
   if (p.seq_q == 1 || g * p.seq_q <= kDecodeMaxRowsPerPass) return GQA_KERNEL_DECODE;
   return GQA_KERNEL_PREFILL;
 }
+
+}  // namespace
 
 int device_sm_count(int* out) {
   int dev = 0;
@@ -120,6 +126,8 @@ int device_sm_count(int* out) {
   *out = sms;
   return GQA_OK;
 }
+
+namespace {
 
 int64_t elem_bytes(const gqa_problem& p) { return p.dtype == GQA_DTYPE_F32 ? 4 : 2; }
 
@@ -298,7 +306,7 @@ GQA_API const char* gqa_status_string(int status) {
 
 GQA_API int gqa_query(const gqa_problem* p, int sm_count, gqa_plan* plan) {
   if (plan == nullptr) return GQA_ERR_NULL;
-  const int rc = validate(p);
+  const int rc = validate_problem(p);
   if (rc != GQA_OK) return rc;
   if (sm_count <= 0) {
     const int drc = device_sm_count(&sm_count);
@@ -310,7 +318,7 @@ GQA_API int gqa_query(const gqa_problem* p, int sm_count, gqa_plan* plan) {
 GQA_API int gqa_forward(const gqa_problem* pp, const void* q, const void* k, const void* v,
                         const uint8_t* mask, void* out, void* workspace, size_t workspace_bytes,
                         void* stream_ptr) {
-  const int rc = validate(pp);
+  const int rc = validate_problem(pp);
   if (rc != GQA_OK) return rc;
   const gqa_problem& p = *pp;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);

@@ -1,0 +1,219 @@
+// C-ABI layer of the 4-bit cache: validation, planning and dispatch of
+// append, read back and attention.  Nothing throws across the ABI.
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "gqa.h"
+#include "kernels.h"
+#include "q4.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int64_t kLim = int64_t(1) << 31;
+
+bool aligned(const void* ptr, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
+}
+
+bool head_dim_ok(int64_t D) { return D >= 8 && D <= 128 && D % 8 == 0; }
+
+// Byte strides of a cache of records: unit inside the record, whole 16-byte
+// pieces over every dimension that is stepped (vector loads and TMA).
+bool cache_strides_ok(const int64_t st[4], const int64_t sizes[3]) {
+  if (st[3] != 1) return false;
+  for (int d = 0; d < 3; ++d)
+    if (st[d] < 0 || (sizes[d] > 1 && st[d] % 16 != 0)) return false;
+  return true;
+}
+
+int validate_q4(const gqa_problem* pp) {
+  if (pp == nullptr) return GQA_ERR_NULL;
+  gqa_problem p = *pp;
+  if (p.dtype == GQA_DTYPE_F32) return GQA_ERR_UNSUPPORTED;
+  // Everything but the caches is checked as for a 16-bit problem of the same sizes.
+  for (int d = 0; d < 4; ++d) p.k_stride[d] = p.v_stride[d] = d == 3 ? 1 : 8;
+  const int rc = validate_problem(&p);
+  if (rc != GQA_OK) return rc;
+  const int64_t sizes[3] = {p.block_table ? p.num_pages : p.batch, p.heads_kv,
+                            p.block_table ? p.page_size : p.seq_k};
+  if (!cache_strides_ok(pp->k_stride, sizes) || !cache_strides_ok(pp->v_stride, sizes))
+    return GQA_ERR_LAYOUT;
+  return GQA_OK;
+}
+
+int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
+  (void)sm_count;
+  std::memset(plan, 0, sizeof(*plan));
+  const int64_t qo = p.batch * p.heads_q * p.seq_q * p.head_dim * 2;
+  const int64_t kv = p.batch * p.heads_kv * p.seq_k * q4::record_bytes(static_cast<int>(p.head_dim));
+  plan->algorithmic_bytes = 2 * qo + 2 * kv + (p.has_mask ? p.batch * p.seq_q * p.seq_k : 0);
+  plan->algorithmic_flops = 4.0 * double(p.batch) * double(p.heads_q) * double(p.seq_q) *
+                            double(p.seq_k) * double(p.head_dim) * (p.causal ? 0.5 : 1.0);
+  plan->workspace_bytes = kWorkspaceHeadBytes;
+  if (p.batch == 0 || p.seq_q == 0) {
+    plan->kernel = GQA_KERNEL_NONE;
+  } else if (p.seq_k == 0 || nothing_visible(p)) {
+    plan->kernel = p.seq_k == 0 ? GQA_KERNEL_ZERO : GQA_KERNEL_NAN;
+    plan->grid = 592;
+    plan->block = 256;
+    plan->launches = 1;
+  } else {
+    plan->kernel = GQA_KERNEL_Q4;
+    const int64_t rows = p.batch * p.heads_q * p.seq_q;
+    plan->grid = static_cast<int32_t>((rows + 7) / 8);
+    plan->block = 256;
+    plan->launches = 1;
+    plan->work_units = static_cast<int32_t>(rows);
+  }
+  return GQA_OK;
+}
+
+// Checks shared by append and read back, and the arguments of both kernels.
+int make_rows_args(const gqa_kv_q4_desc* d, void* cache_k, void* cache_v, void* k, void* v,
+                   const int32_t* lens, void* workspace, size_t workspace_bytes, bool append,
+                   Q4RowsArgs* out) {
+  if (d == nullptr) return GQA_ERR_NULL;
+  if (d->dtype == GQA_DTYPE_F32) return GQA_ERR_UNSUPPORTED;
+  if (d->dtype != GQA_DTYPE_BF16 && d->dtype != GQA_DTYPE_F16) return GQA_ERR_ARG;
+  if (d->batch < 0 || d->heads_kv <= 0 || d->capacity < 0 || d->head_dim <= 0 || d->n < 0 ||
+      d->batch >= kLim || d->heads_kv >= kLim || d->capacity >= kLim || d->n >= kLim)
+    return GQA_ERR_SHAPE;
+  if (!head_dim_ok(d->head_dim)) return GQA_ERR_UNSUPPORTED;
+  if (append ? (d->start != 0 || d->starts != nullptr) : (d->advance != 0 || d->counts != nullptr))
+    return GQA_ERR_ARG;
+  if (append && d->counts == nullptr && d->n > d->capacity) return GQA_ERR_SHAPE;
+  if (!append && (d->start < 0 || d->start >= kLim)) return GQA_ERR_ARG;
+  if (d->block_table != nullptr &&
+      (d->page_size < 1 || d->block_table_stride < 1 || d->num_pages < 1 ||
+       d->page_size >= kLim || d->block_table_stride >= kLim || d->num_pages >= kLim ||
+       d->capacity > d->block_table_stride * d->page_size))
+    return GQA_ERR_SHAPE;
+  const int64_t csz[3] = {d->block_table ? d->num_pages : d->batch, d->heads_kv,
+                          d->block_table ? d->page_size : d->capacity};
+  if (!cache_strides_ok(d->cache_k_stride, csz) || !cache_strides_ok(d->cache_v_stride, csz))
+    return GQA_ERR_LAYOUT;
+  const int64_t* rst[2] = {d->k_stride, d->v_stride};
+  for (const int64_t* s : rst)
+    if (s[3] != 1 || s[0] < 0 || s[1] < 0 || s[2] < 0) return GQA_ERR_LAYOUT;
+  Q4RowsArgs& a = *out;
+  a = Q4RowsArgs{};
+  a.B = static_cast<int>(d->batch);
+  a.n = static_cast<int>(d->n);
+  if (d->batch == 0 || d->n == 0) return GQA_OK;
+  // The kernels count 16-byte pieces of rows in 32 bits.
+  const int64_t per = 8 * q4::groups_of(static_cast<int>(d->head_dim));
+  if (d->batch * d->heads_kv >= kLim / per || d->batch * d->heads_kv * per >= kLim / d->n)
+    return GQA_ERR_UNSUPPORTED;
+  if (cache_k == nullptr || cache_v == nullptr || k == nullptr || v == nullptr ||
+      (append && lens == nullptr))
+    return GQA_ERR_NULL;
+  if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < 256)
+    return GQA_ERR_WORKSPACE;
+  if (!aligned(cache_k, 16) || !aligned(cache_v, 16) || !aligned(k, 2) || !aligned(v, 2) ||
+      !aligned(lens, 4))
+    return GQA_ERR_LAYOUT;
+  a.cache[0] = static_cast<uint8_t*>(cache_k);
+  a.cache[1] = static_cast<uint8_t*>(cache_v);
+  a.rows[0] = static_cast<uint16_t*>(k);
+  a.rows[1] = static_cast<uint16_t*>(v);
+  a.vec = aligned(k, 16) && aligned(v, 16);
+  const int64_t rsz[3] = {d->batch, d->heads_kv, d->n};
+  for (int i = 0; i < 3; ++i) {
+    a.cs[0][i] = d->cache_k_stride[i];
+    a.cs[1][i] = d->cache_v_stride[i];
+    a.rs[0][i] = d->k_stride[i];
+    a.rs[1][i] = d->v_stride[i];
+    if (rsz[i] > 1 && (d->k_stride[i] % 8 != 0 || d->v_stride[i] % 8 != 0)) a.vec = false;
+  }
+  a.lens = const_cast<int32_t*>(lens);  // written by an advancing append only
+  a.counts = d->counts;
+  a.starts = d->starts;
+  a.start = d->start;
+  a.err = static_cast<uint32_t*>(workspace);
+  a.ticket = static_cast<uint32_t*>(workspace) + 1;
+  a.H = static_cast<int>(d->heads_kv);
+  a.D = static_cast<int>(d->head_dim);
+  a.advance = d->advance != 0;
+  a.cap = d->capacity;
+  a.bt = d->block_table;
+  a.bt_stride = d->block_table_stride;
+  a.page_size = d->page_size;
+  a.num_pages = d->num_pages;
+  return GQA_OK;
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+GQA_API int64_t gqa_q4_record_bytes(int64_t head_dim) {
+  return head_dim_ok(head_dim) ? q4::record_bytes(static_cast<int>(head_dim)) : 0;
+}
+
+GQA_API int gqa_kv_append_q4(const gqa_kv_q4_desc* d, void* cache_k, void* cache_v,
+                             const void* k_new, const void* v_new, int32_t* kv_lens,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  Q4RowsArgs a;
+  const int rc = make_rows_args(d, cache_k, cache_v, const_cast<void*>(k_new),
+                                const_cast<void*>(v_new), kv_lens, workspace, workspace_bytes,
+                                true, &a);
+  if (rc != GQA_OK || a.B == 0 || a.n == 0) return rc;
+  return launch_q4_append(a, d->dtype == GQA_DTYPE_F16, static_cast<cudaStream_t>(stream));
+}
+
+GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const void* cache_v,
+                           void* k, void* v, const int32_t* kv_lens, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  Q4RowsArgs a;
+  const int rc = make_rows_args(d, const_cast<void*>(cache_k), const_cast<void*>(cache_v), k, v,
+                                kv_lens, workspace, workspace_bytes, false, &a);
+  if (rc != GQA_OK || a.B == 0 || a.n == 0) return rc;
+  return launch_q4_read(a, d->dtype == GQA_DTYPE_F16, static_cast<cudaStream_t>(stream));
+}
+
+GQA_API int gqa_query_q4(const gqa_problem* p, int sm_count, gqa_plan* plan) {
+  if (plan == nullptr) return GQA_ERR_NULL;
+  const int rc = validate_q4(p);
+  if (rc != GQA_OK) return rc;
+  if (sm_count <= 0) {
+    const int drc = device_sm_count(&sm_count);
+    if (drc != GQA_OK) return drc;
+  }
+  return fill_plan_q4(*p, sm_count, plan);
+}
+
+GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cache_k,
+                           const void* cache_v, const uint8_t* mask, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream_ptr) {
+  const int rc = validate_q4(pp);
+  if (rc != GQA_OK) return rc;
+  const gqa_problem& p = *pp;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  int sms = 0;
+  const int drc = device_sm_count(&sms);
+  if (drc != GQA_OK) return drc;
+  gqa_plan plan;
+  const int prc = fill_plan_q4(p, sms, &plan);
+  if (prc != GQA_OK) return prc;
+  if (plan.kernel == GQA_KERNEL_NONE) return GQA_OK;
+  if (out == nullptr) return GQA_ERR_NULL;
+  if (plan.kernel == GQA_KERNEL_ZERO || plan.kernel == GQA_KERNEL_NAN)
+    return launch_zero(p, out, stream, plan.kernel == GQA_KERNEL_NAN);
+  if (q == nullptr || cache_k == nullptr || cache_v == nullptr) return GQA_ERR_NULL;
+  if (p.has_mask && mask == nullptr) return GQA_ERR_NULL;
+  if (workspace == nullptr || !aligned(workspace, 256) ||
+      workspace_bytes < static_cast<size_t>(plan.workspace_bytes))
+    return GQA_ERR_WORKSPACE;
+  if (!aligned(q, 16) || !aligned(cache_k, 16) || !aligned(cache_v, 16) || !aligned(out, 16))
+    return GQA_ERR_LAYOUT;
+  return launch_q4_rows(p, q, static_cast<const uint8_t*>(cache_k),
+                        static_cast<const uint8_t*>(cache_v), mask, out,
+                        static_cast<uint32_t*>(workspace), stream);
+}
+
+}  // extern "C"

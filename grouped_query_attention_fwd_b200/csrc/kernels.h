@@ -9,6 +9,11 @@
 
 namespace gqa {
 
+// ------------------------------------------------------------ checks shared by the entry points
+int validate_problem(const gqa_problem* p);       // sizes, strides, scalars (api.cu)
+bool nothing_visible(const gqa_problem& p);       // causal / window hide every key from every query
+int device_sm_count(int* out);                    // SMs of the current device, or GQA_ERR_DEVICE
+
 // ------------------------------------------------------------ decode
 // Keys per streamed tile and consumer warps per CTA of the decode kernel.
 constexpr int kDecodeKeysPerTile = 128;
@@ -227,6 +232,32 @@ struct AppendArgs {
 };
 
 int launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+
+// ------------------------------------------------------------ 4-bit cache
+// Writing records (append) and reading them back.
+struct Q4RowsArgs {
+  uint8_t* cache[2];        // K records, V records
+  uint16_t* rows[2];        // 16-bit K rows, V rows: read by append, written by read
+  int64_t cs[2][3];         // byte strides over (b or page, h, row) of the caches
+  int64_t rs[2][3];         // element strides over (b, h, t) of the rows
+  int32_t* lens;            // append: read, then advanced if `advance`; read: valid rows, or nullptr
+  const int32_t* counts;    // append: new rows of each entry, or nullptr (all n)
+  const int32_t* starts;    // read: first row of each entry, or nullptr (start)
+  int64_t start;
+  uint32_t* err;
+  uint32_t* ticket;         // CTAs done (advance only); zero between launches
+  int B, H, D, n, advance;
+  int64_t cap;
+  const int32_t* bt;        // paged cache: block table, or nullptr
+  int64_t bt_stride, page_size, num_pages;
+  bool vec;                 // every 16-bit row starts on 16 bytes
+};
+int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
+int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
+
+// Attention over records: one warp per output row.
+int launch_q4_rows(const gqa_problem& p, const void* q, const uint8_t* k, const uint8_t* v,
+                   const uint8_t* mask, void* out, uint32_t* err, cudaStream_t stream);
 
 // ------------------------------------------------------------ fill: zeros (seq_k == 0) or NaN
 int launch_zero(const gqa_problem& p, void* out, cudaStream_t stream, bool nan);

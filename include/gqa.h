@@ -118,6 +118,7 @@ extern "C" {
 #define GQA_KERNEL_F32 3      /* fp32 CUDA-core path */
 #define GQA_KERNEL_ZERO 4     /* seq_k == 0: the output is filled with zeros */
 #define GQA_KERNEL_NAN 5      /* causal / window leave no key to any query: NaN (see above) */
+#define GQA_KERNEL_Q4 6       /* gqa_forward_q4: attention straight from the 4-bit records */
 
 /* One attention problem.  Strides are in elements. */
 typedef struct gqa_problem {
@@ -281,6 +282,100 @@ typedef struct gqa_kv_append_desc {
 GQA_API int gqa_kv_append(const gqa_kv_append_desc* d, void* cache_k, void* cache_v,
                           const void* k_new, const void* v_new, int32_t* kv_lens,
                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------- 4-bit cache
+ *
+ * A KV cache held in 4 bits: decoding reads the whole cache once per token
+ * ("Multi-Query Attention", "Theory"), so its bytes set the time, and a record
+ * of 4-bit codes holds 128 values in 80 bytes instead of 256.  The pages have
+ * no counterpart.
+ *
+ * Record: one token of one kv head, K or V.  The head_dim values form groups
+ * of GQA_Q4_GROUP (the last may be shorter); a record is
+ * gqa_q4_record_bytes(head_dim) = 16 * (1 + groups) bytes:
+ *   bytes [4 g, 4 g + 4)        group g's scale, then its minimum, both in the
+ *                               cache's 16-bit type; [4 * groups, 16) zero
+ *   bytes [16 + 16 g, 32 + 16 g) group g's codes: value 32 g + i in the low
+ *                               (i even) or high (i odd) half of byte i / 2;
+ *                               codes past head_dim are zero
+ * Written from 16-bit values x (fp32 arithmetic, rounding to nearest even):
+ *   minimum = min x,  scale = round16((max x - minimum) / 15),
+ *   code = min(15, rint((x - minimum) / scale)), 0 where scale is 0
+ * and read as scale * code + minimum.  The minimum is exact, and a value is
+ * off by at most half a step (a step at the top end, where round16 shortened
+ * the scale).  A group with a NaN or an infinity, or whose max - min overflows
+ * fp32, gets scale = minimum = NaN and reads back NaN throughout.
+ *
+ * Caches: k and v are uint8 [batch, heads_kv, capacity, record] or, with a
+ * block table, pools [num_pages, heads_kv, page_size, record].  Their strides
+ * are in BYTES; the record's own stride is 1, the base and every stride of a
+ * dimension longer than 1 are multiples of 16.  dtype is BF16 or F16: the type
+ * of the rows written and read back, of q and out, and of scale and minimum.
+ */
+#define GQA_Q4_GROUP 32
+
+/* Bytes of one record; 0 for a head_dim that is not a multiple of 8 in [8, 128]. */
+GQA_API int64_t gqa_q4_record_bytes(int64_t head_dim);
+
+/* Rows written to (gqa_kv_append_q4) or read from (gqa_kv_read_q4) a 4-bit cache. */
+typedef struct gqa_kv_q4_desc {
+  int32_t dtype;              /* GQA_DTYPE_BF16 or GQA_DTYPE_F16 */
+  int32_t advance;            /* append: nonzero adds the new rows to kv_lens; read: must be 0 */
+  int64_t batch, heads_kv, capacity, head_dim;
+  int64_t n;                  /* rows of k and v per entry */
+  int64_t cache_k_stride[4];  /* bytes, over (b or page, h_kv, row, byte) */
+  int64_t cache_v_stride[4];
+  int64_t k_stride[4];        /* elements, over (b, h_kv, t, d), t < n; d stride 1 */
+  int64_t v_stride[4];
+  const int32_t* counts;      /* append: NULL (n each), or device [batch]: rows t < counts[b] only */
+  const int32_t* starts;      /* read: NULL (start each), or device [batch]: first row read */
+  int64_t start;              /* read: first row, where starts is NULL; append: must be 0 */
+  const int32_t* block_table; /* NULL, or device [batch, block_table_stride] as in gqa_problem */
+  int64_t block_table_stride, page_size, num_pages;
+} gqa_kv_q4_desc;
+
+/*
+ * gqa_kv_append_q4 -- quantise the rows k_new[b, :, t, :] and v_new, t < n (or
+ * counts[b]), into records kv_lens[b] + t of the cache, as gqa_kv_append does
+ * with 16-bit rows.  With `advance`, kv_lens[b] then grows by that number;
+ * without, the lengths stay, so that several layers can share one tensor of
+ * lengths.  An entry whose rows do not fit the capacity, or whose count is
+ * outside [0, n], is left unchanged and reported as GQA_ERR_KV_LENGTH.  A row
+ * whose page index is outside [0, num_pages) is not written, its entry's
+ * length is not advanced, and GQA_ERR_PAGE is reported.  Records of other rows
+ * are left as they were.  No two rows may go to the same record.
+ *   workspace: as for gqa_kv_append (256 bytes, zero-filled before its first
+ *              use).  Asynchronous; one launch.
+ */
+GQA_API int gqa_kv_append_q4(const gqa_kv_q4_desc* d, void* cache_k, void* cache_v,
+                             const void* k_new, const void* v_new, int32_t* kv_lens,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * gqa_kv_read_q4 -- k[b, :, t, :] and v[b, :, t, :], t < n, from records
+ * start + t (starts[b] + t) of the cache, rounded once to the 16-bit type.
+ * Rows at or past the entry's length (kv_lens[b], or the capacity without
+ * kv_lens) are zeros.  A length outside [0, capacity] is clamped and a
+ * negative start reads zeros, both reported as GQA_ERR_KV_LENGTH; a page index
+ * outside [0, num_pages) reads zeros and is reported as GQA_ERR_PAGE.
+ * Asynchronous; one launch; workspace as above.
+ */
+GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const void* cache_v,
+                           void* k, void* v, const int32_t* kv_lens, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * gqa_query_q4, gqa_forward_q4 -- gqa_query and gqa_forward over a 4-bit
+ * cache: q and out as there (dtype BF16 or F16), k and v the records, with
+ * k_stride and v_stride in bytes.  Masks, causal_offset, window, kv_lens,
+ * paged caches, empty problems, rows without a visible key, the workspace and
+ * the errors are those of gqa_forward.
+ */
+GQA_API int gqa_query_q4(const gqa_problem* p, int sm_count, gqa_plan* plan);
+GQA_API int gqa_forward_q4(const gqa_problem* p, const void* q, const void* cache_k,
+                           const void* cache_v, const uint8_t* mask, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /*
  * gqa_debug_decode_trace -- diagnostics: record per-CTA phase timestamps of
