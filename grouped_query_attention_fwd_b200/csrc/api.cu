@@ -189,6 +189,8 @@ int fill_plan(const gqa_problem& p, int sm_count, gqa_plan* plan) {
 
 // ------------------------------------------------------------ TMA descriptors
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (fn == nullptr) {
@@ -204,6 +206,8 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
   }
   return fn;
 }
+
+namespace {
 
 // 4-D bf16 map over (d, s, h, b) of a tensor with element strides st[0..2]
 // for (b, h, s); box {64, box_s, box_h, 1} with 128-byte swizzle.

@@ -60,14 +60,46 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
     plan->block = 256;
     plan->launches = 1;
   } else {
+    const DecodeShape s = plan_decode_q4(p, sm_count);
+    if (s.units >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit unit indices
     plan->kernel = GQA_KERNEL_Q4;
-    const int64_t rows = p.batch * p.heads_q * p.seq_q;
-    plan->grid = static_cast<int32_t>((rows + 7) / 8);
-    plan->block = 256;
-    plan->launches = 1;
-    plan->work_units = static_cast<int32_t>(rows);
+    plan->grid = s.grid;
+    plan->block = decode_q4_threads(s);
+    plan->smem_bytes = s.smem_bytes;
+    plan->launches = s.zero_counters ? 2 : 1;
+    plan->work_units = static_cast<int32_t>(s.units);
+    plan->workspace_bytes = (s.workspace_end + 255) / 256 * 256;
   }
   return GQA_OK;
+}
+
+// Tensor map over (byte, row, kv head, entry or page) of a cache of records:
+// boxes of `rows` records, padded with zeros to the kernel's record size.
+int encode_records(CUtensorMap* map, const void* base, const gqa_problem& p, const int64_t st[4],
+                   int padded_dim) {
+  auto enc = get_encoder();
+  if (enc == nullptr) return GQA_ERR_CUDA;
+  const bool paged = p.block_table != nullptr;
+  const int64_t bytes = q4::record_bytes(static_cast<int>(p.head_dim));
+  const int64_t S = paged ? p.page_size : p.seq_k, H = p.heads_kv;
+  const int64_t B = paged ? p.num_pages : p.batch;
+  // Strides of length-1 dimensions are never stepped; give them a legal value.
+  const int64_t sb = S > 1 ? st[2] : bytes;
+  const int64_t hb = H > 1 ? st[1] : sb * S;
+  const int64_t bb = B > 1 ? st[0] : hb * H;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(bytes), static_cast<cuuint64_t>(S),
+                              static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(sb), static_cast<cuuint64_t>(hb),
+                                 static_cast<cuuint64_t>(bb)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(q4::record_bytes(padded_dim)),
+                             static_cast<cuuint32_t>(paged ? kDecodePageBox : kDecodeKeysPerTile),
+                             1, 1};
+  const cuuint32_t unit[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box,
+             unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? GQA_OK
+             : GQA_ERR_LAYOUT;
 }
 
 // Checks shared by append and read back, and the arguments of both kernels.
@@ -211,9 +243,22 @@ GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cac
     return GQA_ERR_WORKSPACE;
   if (!aligned(q, 16) || !aligned(cache_k, 16) || !aligned(cache_v, 16) || !aligned(out, 16))
     return GQA_ERR_LAYOUT;
-  return launch_q4_rows(p, q, static_cast<const uint8_t*>(cache_k),
-                        static_cast<const uint8_t*>(cache_v), mask, out,
-                        static_cast<uint32_t*>(workspace), stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const DecodeShape s = plan_decode_q4(p, sms);
+  CUtensorMap tmk, tmv;
+  int erc = encode_records(&tmk, cache_k, p, p.k_stride, s.D);
+  if (erc != GQA_OK) return erc;
+  erc = encode_records(&tmv, cache_v, p, p.v_stride, s.D);
+  if (erc != GQA_OK) return erc;
+  const DecodeArgs a = make_decode_args(p, s, q, mask, out, ws);
+  // The ticket counters must start at zero; past their region of the
+  // workspace other calls may have left bytes.
+  if (s.zero_counters &&
+      cudaMemsetAsync(a.counters, 0, static_cast<size_t>(s.groups) * 4, stream) != cudaSuccess) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  return launch_decode_q4(p, s, a, tmk, tmv, stream);
 }
 
 }  // extern "C"

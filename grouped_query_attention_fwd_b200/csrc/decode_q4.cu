@@ -1,0 +1,798 @@
+// Decode over a 4-bit cache: split-K attention that reads the records once.
+//
+// One token (or a short query block) attends to keys held as records: per
+// group of 32 values a scale s, a minimum m and 4-bit codes c.  Nothing is
+// expanded in memory, and no value is rounded to 16 bits on the way:
+//
+//   q . K_j   = sum_g  s_jg (q_g . c_jg) + m_jg sum(q_g)
+//   out       = sum_j  (p_j s_jg) c_jg   +  sum_j p_j m_jg        per group g
+//
+// The two products over codes run on the tensor cores (warp-level MMAs: the
+// operands come out of registers, where the codes are unpacked), everything
+// with a scale or a minimum in fp32.
+//
+//  * Codes as operands: a nibble in bits 0-3 or 4-7 of a 16-bit half is, read
+//    as bf16 or fp16, a subnormal (or first-binade) number, linear in the
+//    code: c or 16 c times the type's smallest step.  One AND per two codes
+//    makes an operand register, one shift per word brings the upper byte down:
+//    5 instructions per 8 codes.  The 16 is undone in Q (its odd dims are
+//    scaled by 1/16) or in the output rows.  Q is scaled by a power of two so
+//    that the products stay inside fp32's normal range (bf16: 2^64; fp16: so
+//    that each head's largest element is in [2^14, 2^15)).
+//  * S^T = C_K Q^T with 16 keys of a chunk in M: a thread's 32-bit word of a
+//    K record holds eight consecutive dims of one key, which are just the k
+//    indices that its fragments want when Q uses the same order.  For V,
+//    ldmatrix.trans of the 16-byte code blocks pairs the same halfword of two
+//    keys in one register, the layout of V^T as the A operand.
+//  * The weights p_j s_jg are rounded to fp16 (2^-11) as the B operand of
+//    P V in both cache types.  To keep them in fp16's range whatever the
+//    scales, the exponent reference is the running maximum of t_j + log2 of
+//    key j's largest V scale: the weights stay at or below 2^8.  An fp16 cache
+//    also counts its V codes from 8 (one packed subtraction per register), so
+//    that the rounding multiplies at most half of the group's range; bf16
+//    outputs are rounded 8 times more coarsely than the weights as it is.
+//  * The reference is lazy: it moves, and the sums are rescaled, only when a
+//    score passes it by more than 2^8, which one vote per chunk finds out.
+//
+// Bound: HBM, at 160 bytes per key of 128 dims against 512 in 16 bits; the
+// unpacking fills about half of the ALU issue slots that this leaves.  Work is
+// cut into ranges of 128-key units as in the 16-bit decode; a producer warp
+// streams K and V records with TMA into a ring, W consumer warps take 16-key
+// chunks in turn, and each keeps a softmax state of its own until the group
+// ends.  80-byte (48-byte) rows make every ldmatrix and parameter read free of
+// bank conflicts without a swizzle.
+#include <cuda_runtime.h>
+
+#include "decode_sched.cuh"
+#include "epilogue.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+#include "q4.cuh"
+
+namespace gqa {
+namespace {
+
+using namespace q4;
+
+constexpr int KT = kDecodeKeysPerTile;
+constexpr int kChunk = 16;                 // keys a warp takes at a time
+constexpr int kChunks = KT / kChunk;
+constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
+
+template <int NG, int NT>
+struct Q4Layout {
+  static constexpr int D = NG * kGroup;            // head_dim, padded
+  static constexpr int HP = 8 * NT;                // rows per pass
+  static constexpr int W = NT == 1 ? 11 : 7;       // consumer warps: 3 (2) per scheduler with the producer
+  static constexpr int kThreads = (W + 1) * 32;
+  static constexpr int kPitch = record_bytes(D);   // bytes per record in shared memory
+  static constexpr int kTile = KT * kPitch;        // K (or V) records of a unit
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kRow = D + 4;               // a row's O, then (m, l), padded (floats)
+  static constexpr int kScratch = W * HP * kRow * 4;
+  static int bytes(int stages, int ragged_batch) {
+    return 128 /*alignment slack*/ + stages * kStage + kScratch + 2 * stages * 8 + 16 +
+           (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
+  }
+};
+
+// D = A B, no accumulator.
+template <bool F16>
+__device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float fast_lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// V codes of two keys as an A register: bits 0-3 (or 4-7, times 16) of each
+// half; for an fp16 cache counted from 8 (-8 and -128 smallest fp16 steps).
+template <bool F16>
+__device__ __forceinline__ uint32_t v_codes_lo(uint32_t x) {
+  const uint32_t c = x & 0x000F000Fu;
+  return F16 ? hadd2(c, 0x80088008u) : c;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t v_codes_hi(uint32_t x) {
+  const uint32_t c = x & 0x00F000F0u;
+  return F16 ? hadd2(c, 0x80808080u) : c;
+}
+
+// Record heads: NG words (scale | minimum << 16).
+template <int NG>
+__device__ __forceinline__ void load_params(uint32_t (&w)[NG], uint32_t addr) {
+  if (NG == 4)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[NG - 2]), "=r"(w[NG - 1])
+                 : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+
+// MQ: several query positions per kv head; row r = head * seq_q + query.
+template <int NG, int NT, bool MQ, bool F16>
+__global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
+    gqa_decode_q4_kernel(const __grid_constant__ CUtensorMap tmk,
+                         const __grid_constant__ CUtensorMap tmv, const DecodeArgs a,
+                         const int tiles_per_group, const int passes, const int units,
+                         const int stages, uint32_t* __restrict__ counters) {
+  using L = Q4Layout<NG, NT>;
+  constexpr int HP = L::HP, D = L::D, W = L::W, P = L::kPitch, R = L::kRow;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                             ~static_cast<uintptr_t>(127));
+  float* scr = reinterpret_cast<float*>(ring + stages * L::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scr) + L::kScratch);
+  uint64_t* empty = full + stages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + stages);
+  volatile int* last_flag = abort_flag + 1;
+  int* len_s = reinterpret_cast<int*>(const_cast<int*>(abort_flag) + 4);
+  int* pre_s = len_s + a.B;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const bool ragged = a.lens != nullptr;
+  const int gpb = a.Hkv * passes;
+
+  if (threadIdx.x == W * 32) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kChunks);  // one arrival per chunk
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // From here on global memory written by earlier work on the stream is read.
+  griddep_wait();
+  griddep_launch_dependents();
+  if (ragged) {
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+      int len = a.lens[b];
+      if (len < 0 || len > a.Sk) {
+        if (blockIdx.x == 0) atomicOr(a.err, kErrKvLength);
+        len = len < 0 ? 0 : a.Sk;
+      }
+      len_s[b] = len;
+    }
+  }
+  __syncthreads();
+  if (ragged) {
+    if (warp == 0) {
+      // pre[b + 1] = sum over entries <= b of (groups per entry) x (tiles of the entry).
+      int carry = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        int v = 0;
+        if (b < a.B)
+          v = gpb * decode_key_range(len_s[b], a.Sk, a.Sq, a.causal, a.causal_offset, a.window)
+                        .tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += n;
+        }
+        if (b < a.B) pre_s[b + 1] = carry + v;
+        carry += __shfl_sync(0xffffffffu, v, 31);
+      }
+      if (lane == 0) pre_s[0] = 0;
+    }
+    __syncthreads();
+  }
+  Sched sc;
+  sc.pre = ragged ? pre_s : nullptr;
+  sc.len = ragged ? len_s : nullptr;
+  sc.per_b = gpb * tiles_per_group;
+  sc.gpb = gpb;
+  sc.B = a.B;
+  sc.total = ragged ? pre_s[a.B] : units;
+  sc.P = static_cast<int>(gridDim.x) < sc.total ? static_cast<int>(gridDim.x) : sc.total;
+  const bool has_range = static_cast<int>(blockIdx.x) < sc.P;
+  const int u_begin = has_range ? range_start(blockIdx.x, sc.total, sc.P) : 0;
+  const int u_end = has_range ? range_start(blockIdx.x + 1, sc.total, sc.P) : 0;
+
+  if (warp == W) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int it = 0;
+      Cursor cu;
+      for (int u = u_begin; u < u_end; ++u, ++it) {
+        const int s = it % stages;
+        const uint32_t round = static_cast<uint32_t>(it / stages);
+        if (round > 0 &&
+            !mbar_wait(&empty[s], (round & 1u) ^ 1u, abort_flag, a.err, kErrDecodeWait, a.wait_ns))
+          break;
+        if (u == a.withhold_unit) {  // test of the bounded waits, as in the 16-bit decode
+          const uint64_t t0 = globaltimer_ns();
+          while (!*abort_flag && globaltimer_ns() - t0 < 4 * a.wait_ns) {
+          }
+          break;
+        }
+        seek(cu, u, sc, a);
+        const int r = u - cu.beg;
+        const int gi = r / cu.kr.tiles;
+        const int key0 = (r - gi * cu.kr.tiles + cu.kr.t0) * KT;
+        const int kv = gi / passes, b = cu.b;
+        uint8_t* st = ring + s * L::kStage;
+        mbar_arrive_expect_tx(&full[s], L::kStage);
+        if (a.bt != nullptr) {
+          // Two 64-key boxes, each inside one page; one past the sequence's
+          // length takes page num_pages, which TMA fills with zeros.
+          const int len = sc.len ? sc.len[b] : a.Sk;
+#pragma unroll
+          for (int h = 0; h < KT / kDecodePageBox; ++h) {
+            const int key = key0 + h * kDecodePageBox;
+            int page = a.num_pages;
+            if (key < len) {
+              page = __ldg(a.bt + b * a.bt_stride + key / a.page_size);
+              if (page < 0 || page >= a.num_pages) {
+                atomicOr(a.err, kErrPage);
+                page = a.num_pages;  // read as zeros
+              }
+            }
+            uint8_t* dst = st + h * kDecodePageBox * P;
+            tma_load_4d(dst, &tmk, &full[s], 0, key % a.page_size, kv, page);
+            tma_load_4d(dst + L::kTile, &tmv, &full[s], 0, key % a.page_size, kv, page);
+          }
+        } else {
+          tma_load_4d(st, &tmk, &full[s], 0, key0, kv, b);
+          tma_load_4d(st + L::kTile, &tmv, &full[s], 0, key0, kv, b);
+        }
+      }
+      // Unwind: no copy may still be landing in this CTA's shared memory.
+      if (*abort_flag)
+        for (int j = it > stages ? it - stages : 0; j < it; ++j)
+          mbar_wait_drain(&full[j % stages], static_cast<uint32_t>((j / stages) & 1),
+                          a.wait_ns / 4);
+    }
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int c = lane & 3, r8 = lane >> 2;
+    auto sync_consumers = [] { asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory"); };
+    Cursor cu;
+    for (int ua = u_begin; ua < u_end;) {
+      // One group (kv head and pass of one entry): units [ua, ub) of this range.
+      seek(cu, ua, sc, a);
+      const int gi = (ua - cu.beg) / cu.kr.tiles;
+      const int grp_beg = cu.beg + gi * cu.kr.tiles;
+      const int grp_tiles = cu.kr.tiles;
+      const int ub = min(u_end, grp_beg + grp_tiles);
+      const int tile0 = ua - grp_beg + cu.kr.t0;
+      const int kv = gi / passes, pass = gi % passes, b = cu.b;
+      const int len = sc.len ? sc.len[b] : a.Sk;
+      const int grp = b * gpb + gi;
+
+      // Q as B fragments, thread (r8, c): row r8 of each column tile, dims
+      // 32 t + 8 c .. + 7; sums over each group's dims for the minima.
+      uint32_t bq[NT][NG][4];
+      float qs[NT][NG][2], fac[NT][2];
+      int vlo[NT][2], vhi[NT][2];          // visible keys of this thread's two rows (MQ)
+      const uint8_t* vmask[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int hl = pass * HP + nt * 8 + r8;
+        const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
+        const uint16_t* qrow = a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
+                               static_cast<int64_t>(qi) * a.qs[2];
+        float f[NG][8];
+        float amax = 0.f;
+#pragma unroll
+        for (int t = 0; t < NG; ++t) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (hl < a.rows && 32 * t + 8 * c < a.Dv)
+            x = *reinterpret_cast<const uint4*>(qrow + 32 * t + 8 * c);
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            f[t][2 * i] = to_f32<F16>(w[i] & 0xFFFFu);
+            f[t][2 * i + 1] = to_f32<F16>(w[i] >> 16);
+            amax = fmaxf(amax, fmaxf(fabsf(f[t][2 * i]), fabsf(f[t][2 * i + 1])));
+          }
+        }
+        // Power of two that Q is scaled by, and what the scores then lack
+        // (the codes' own step is 2^-133 in bf16, 2^-24 in fp16).
+        float up, back;
+        if (F16) {
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+          const int e = amax > 0.f && ex < 16 ? 14 - ex : 0;
+          up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+          back = __uint_as_float(static_cast<uint32_t>(127 + 24 - e) << 23);
+        } else {
+          up = 0x1p64f;
+          back = 0x1p69f;
+        }
+        float sums[NG];
+#pragma unroll
+        for (int t = 0; t < NG; ++t) {
+          float s = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s += f[t][i];
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          sums[t] = s / back;  // a power of two: exact
+          const float odd = up * 0.0625f;
+          bq[nt][t][0] = pack2<F16>(f[t][0] * up, f[t][4] * up);
+          bq[nt][t][1] = pack2<F16>(f[t][1] * odd, f[t][5] * odd);
+          bq[nt][t][2] = pack2<F16>(f[t][2] * up, f[t][6] * up);
+          bq[nt][t][3] = pack2<F16>(f[t][3] * odd, f[t][7] * odd);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int src = (2 * c + e) * 4;
+#pragma unroll
+          for (int t = 0; t < NG; ++t) qs[nt][t][e] = __shfl_sync(0xffffffffu, sums[t], src);
+          fac[nt][e] = a.scale_log2 * __shfl_sync(0xffffffffu, back, src);
+          const int row = pass * HP + nt * 8 + 2 * c + e;
+          const int i = MQ ? (row < a.rows ? row : 0) % a.Sq : 0;
+          vlo[nt][e] = cu.kr.lo;
+          vhi[nt][e] = cu.kr.hi;
+          if (MQ) {
+            const int64_t top = i + a.causal_offset + (len - a.Sk);  // query i's diagonal
+            int64_t lo = 0, hi = len;
+            if (a.causal) {
+              hi = top + 1 < hi ? top + 1 : hi;
+              if (a.window > 0 && top - a.window + 1 > 0) lo = top - a.window + 1;
+            }
+            vlo[nt][e] = static_cast<int>(lo < len ? lo : len);
+            vhi[nt][e] = static_cast<int>(hi > 0 ? hi : 0);
+          }
+          vmask[nt][e] =
+              a.mask ? a.mask + b * a.ms[0] + static_cast<int64_t>(i) * a.ms[1] : nullptr;
+        }
+      }
+      // Keys that every row sees (without a mask): the first query's upper
+      // limit, the last query's lower one.
+      int all_lo = cu.kr.lo, all_hi = cu.kr.hi;
+      if (MQ && a.causal) {
+        const int64_t top0 = a.causal_offset + (len - a.Sk);
+        all_hi = static_cast<int>(top0 + 1 < 0 ? 0 : (top0 + 1 < len ? top0 + 1 : len));
+        if (a.window > 0) {
+          const int64_t lo = top0 + a.Sq - a.window;
+          all_lo = static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
+        }
+      }
+
+      float o[NT][NG][2][4], corr[NT][NG][2];
+      float m_ref[NT][2], l[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m_ref[nt][e] = -INFINITY;
+          l[nt][e] = 0.f;
+#pragma unroll
+          for (int t = 0; t < NG; ++t) {
+            corr[nt][t][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[nt][t][e][x] = 0.f;
+          }
+        }
+
+      // Chunks of the CTA's range are numbered through; warp w takes those
+      // that are w modulo W.
+      const int x0 = (ua - u_begin) * kChunks, x1 = (ub - u_begin) * kChunks;
+      int x = x0 + (warp - x0 % W + W) % W;
+      int s = (x / kChunks) % stages;
+      uint32_t parity = static_cast<uint32_t>((x / kChunks) / stages) & 1u;
+      for (int it = x / kChunks; x < x1; x += W) {
+        for (; it < x / kChunks; ++it)
+          if (++s == stages) {
+            s = 0;
+            parity ^= 1u;
+          }
+        const int chunk = x % kChunks;
+        const int key0 = (tile0 + it - (ua - u_begin)) * KT + chunk * kChunk;
+        const bool landed =
+            mbar_wait(&full[s], parity, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
+        // (A wait that gave up sets the abort flag: the arithmetic is skipped,
+        // the walk goes on, so that all warps reach the same barriers.)
+        const bool work = landed && key0 < cu.kr.hi && key0 + kChunk > cu.kr.lo;
+        if (!__any_sync(0xffffffffu, work)) {
+          if (lane == 0) mbar_arrive(&empty[s]);
+          continue;
+        }
+        const uint32_t kb = smem_u32(ring + s * L::kStage) + chunk * kChunk * P;
+        const uint32_t vb = kb + L::kTile;
+        // Codes and parameters of the chunk's 16 records, K and V.
+        const uint32_t row_at = ((lane >> 3) & 1) * 8 + (lane & 7);
+        const uint32_t at = row_at * P + kHeadBytes + (lane >> 4) * 16;
+        uint32_t kw[NG][2], vw[NG][2];  // [group][keys 0-7 | 8-15]
+#pragma unroll
+        for (int t = 0; t < NG; t += 2)
+          ldmatrix_x4(kw[t][0], kw[t][1], kw[t + 1][0], kw[t + 1][1], kb + at + t * 16);
+        uint32_t kp[2][NG], vp[2][NG];  // [key r8 | r8 + 8][group]
+        load_params<NG>(kp[0], kb + r8 * P);
+        load_params<NG>(kp[1], kb + (r8 + 8) * P);
+#pragma unroll
+        for (int t = 0; t < NG; t += 2)
+          ldmatrix_x4_trans(vw[t][0], vw[t][1], vw[t + 1][0], vw[t + 1][1], vb + at + t * 16);
+        load_params<NG>(vp[0], vb + r8 * P);
+        load_params<NG>(vp[1], vb + (r8 + 8) * P);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);  // the chunk is in registers
+
+        float sv[NT][4];  // scores: keys r8 (0, 1) and r8 + 8 (2, 3), rows 2 c + {0, 1}
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) sv[nt][y] = 0.f;
+#pragma unroll
+        for (int t = 0; t < NG; ++t) {
+          const uint32_t a8 = kw[t][0] >> 8, b8 = kw[t][1] >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4];
+            mma_zero<F16>(acc, kw[t][0] & 0x000F000Fu, kw[t][1] & 0x000F000Fu,
+                          kw[t][0] & 0x00F000F0u, kw[t][1] & 0x00F000F0u, bq[nt][t][0],
+                          bq[nt][t][1]);
+            mma_16816<F16>(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                           b8 & 0x00F000F0u, bq[nt][t][2], bq[nt][t][3]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              sv[nt][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y],
+                               fmaf(min_of<F16>(kp[y >> 1][t]), qs[nt][t][y & 1], sv[nt][y]));
+          }
+        }
+        // log2 of each key's largest V scale (see the top), within 2^-60 .. 2^100.
+        float lsv[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float m = 0x1p-60f;
+#pragma unroll
+          for (int t = 0; t < NG; ++t) m = fmaxf(m, scale_of<F16>(vp[k][t]));
+          lsv[k] = fast_lg2(fminf(m, 0x1p100f));
+        }
+
+        auto rest = [&](auto whole) {
+          constexpr bool kWhole = decltype(whole)::value;
+          // Scores in base 2; hidden keys -inf.
+          bool raise = false;
+          bool seen[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int e = y & 1, key = key0 + r8 + (y >> 1) * 8;
+              float t = sv[nt][y] * fac[nt][e];
+              seen[nt][y] = kWhole || (key >= vlo[nt][e] && key < vhi[nt][e] &&
+                                       mask_allows(vmask[nt][e], key));
+              if (!seen[nt][y]) t = -INFINITY;
+              sv[nt][y] = t;
+              raise |= t + lsv[y >> 1] > m_ref[nt][e] + kLazyLog2;
+            }
+          if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(sv[nt][e] + lsv[0], sv[nt][2 + e] + lsv[1]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float m_new = fmaxf(m_ref[nt][e], mx);
+                const float alpha = fast_exp2(m_ref[nt][e] - exp_ref(m_new));
+                m_ref[nt][e] = m_new;
+                l[nt][e] *= alpha;
+#pragma unroll
+                for (int t = 0; t < NG; ++t) {
+                  corr[nt][t][e] *= alpha;
+#pragma unroll
+                  for (int u = 0; u < 2; ++u) {
+                    o[nt][t][u][e] *= alpha;
+                    o[nt][t][u][2 + e] *= alpha;
+                  }
+                }
+              }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              sv[nt][y] = fast_exp2(sv[nt][y] - exp_ref(m_ref[nt][y & 1]));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) l[nt][e] += sv[nt][e] + sv[nt][2 + e];
+          }
+#pragma unroll
+          for (int t = 0; t < NG; ++t) {
+            const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const float scale = scale_of<F16>(vp[k][t]);
+                float add = min_of<F16>(vp[k][t]);
+                if (F16) add = fmaf(8.f, scale, add);
+                float w0 = sv[nt][2 * k] * scale, w1 = sv[nt][2 * k + 1] * scale;
+                float c0 = sv[nt][2 * k] * add, c1 = sv[nt][2 * k + 1] * add;
+                if (!kWhole) {  // a hidden key's parameters may be NaN
+                  w0 = seen[nt][2 * k] ? w0 : 0.f;
+                  w1 = seen[nt][2 * k + 1] ? w1 : 0.f;
+                  c0 = seen[nt][2 * k] ? c0 : 0.f;
+                  c1 = seen[nt][2 * k + 1] ? c1 : 0.f;
+                }
+                corr[nt][t][0] += c0;
+                corr[nt][t][1] += c1;
+                pb[nt][k] = movmatrix_trans(pack_f16x2(w0, w1));
+              }
+            const uint32_t x0 = v_codes_lo<F16>(vw[t][0]), x1 = v_codes_hi<F16>(vw[t][0]);
+            const uint32_t x2 = v_codes_lo<F16>(vw[t][1]), x3 = v_codes_hi<F16>(vw[t][1]);
+            const uint32_t y0 = v_codes_lo<F16>(v0), y1 = v_codes_hi<F16>(v0);
+            const uint32_t y2 = v_codes_lo<F16>(v1), y3 = v_codes_hi<F16>(v1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16_16816(o[nt][t][0], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
+              mma_f16_16816(o[nt][t][1], y0, y1, y2, y3, pb[nt][0], pb[nt][1]);
+            }
+          }
+        };
+        if (!a.has_mask && key0 >= all_lo && key0 + kChunk <= all_hi)
+          rest(BoolConst<true>{});
+        else
+          rest(BoolConst<false>{});
+      }
+
+      // ---- end of the group: the W warps' states meet in shared memory.
+      float* mine = scr + warp * HP * R;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = nt * 8 + 2 * c + e;
+          float lv = l[nt][e];
+#pragma unroll
+          for (int i = 4; i < 32; i <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, i);
+#pragma unroll
+          for (int t = 0; t < NG; ++t) {
+            float cv = corr[nt][t][e];
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1) cv += __shfl_xor_sync(0xffffffffu, cv, i);
+            // Codes carry 2^-24, those of odd nibbles 2^-20.
+            const float4 ov = make_float4(fmaf(o[nt][t][0][e], 0x1p24f, cv),
+                                          fmaf(o[nt][t][0][2 + e], 0x1p20f, cv),
+                                          fmaf(o[nt][t][1][e], 0x1p24f, cv),
+                                          fmaf(o[nt][t][1][2 + e], 0x1p20f, cv));
+            *reinterpret_cast<float4*>(mine + h * R + 32 * t + 4 * r8) = ov;
+          }
+          if (r8 == 0) *reinterpret_cast<float2*>(mine + h * R + D) = make_float2(m_ref[nt][e], lv);
+        }
+      sync_consumers();
+      const int rows = min(HP, a.rows - pass * HP);
+      const int quads = rows * (D / 4);
+      // Row hr of the pass, dims 4 d4 .. + 3 over the W states: (M, l, O).
+      auto merge_warps = [&](int hr, int d4, float& M, float& lsum, float4& acc) {
+        M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, scr[(w * HP + hr) * R + D]);
+        lsum = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float ref = exp_ref(M);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float* row = scr + (w * HP + hr) * R;
+          const float wt = fast_exp2(row[D] - ref);
+          lsum = fmaf(wt, row[D + 1], lsum);
+          const float4 ov = *reinterpret_cast<const float4*>(row + 4 * d4);
+          acc.x = fmaf(wt, ov.x, acc.x);
+          acc.y = fmaf(wt, ov.y, acc.y);
+          acc.z = fmaf(wt, ov.z, acc.z);
+          acc.w = fmaf(wt, ov.w, acc.w);
+        }
+      };
+      auto write_out = [&](int hr, int d4, float lsum, const float4& acc) {
+        if (4 * d4 >= a.Dv) return;
+        const int row = pass * HP + hr;
+        const int hh = MQ ? row / a.Sq : row, qi = MQ ? row % a.Sq : 0;
+        const float inv = 1.f / lsum;  // no visible key: 0 * inf = NaN
+        uint2 pk;
+        pk.x = pack2<F16>(acc.x * inv, acc.y * inv);
+        pk.y = pack2<F16>(acc.z * inv, acc.w * inv);
+        *reinterpret_cast<uint2*>(a.out + b * a.os[0] +
+                                  static_cast<int64_t>(kv * a.g + hh) * a.os[1] +
+                                  static_cast<int64_t>(qi) * a.os[2] + 4 * d4) = pk;
+      };
+      const int c_lo = cta_of_unit(grp_beg, sc.total, sc.P);
+      const int c_hi = cta_of_unit(grp_beg + grp_tiles - 1, sc.total, sc.P);
+      if (c_lo == c_hi) {
+        for (int i = threadIdx.x; i < quads; i += W * 32) {
+          float M, lsum;
+          float4 acc;
+          merge_warps(i / (D / 4), i % (D / 4), M, lsum, acc);
+          write_out(i / (D / 4), i % (D / 4), lsum, acc);
+        }
+      } else {
+        // Split over several CTAs: publish a partial, take a ticket; the last
+        // of them merges.  Only a range's first and last group can be split:
+        // two partial slots per CTA.
+        auto slot_of = [&](int cta) {
+          const int first = group_of(range_start(cta, sc.total, sc.P), sc, a);
+          return (cta * 2 + (first == grp ? 0 : 1)) * HP;
+        };
+        const int base = slot_of(blockIdx.x);
+        for (int i = threadIdx.x; i < quads; i += W * 32) {
+          const int hr = i / (D / 4), d4 = i % (D / 4);
+          float M, lsum;
+          float4 acc;
+          merge_warps(hr, d4, M, lsum, acc);
+          *reinterpret_cast<float4*>(&a.part_o[static_cast<int64_t>(base + hr) * D + 4 * d4]) = acc;
+          if (d4 == 0) a.part_ml[base + hr] = make_float2(M, lsum);
+        }
+        sync_consumers();
+        const int n = c_hi - c_lo + 1;
+        if (threadIdx.x == 0)
+          *last_flag = atom_add_acq_rel_gpu(&counters[grp], 1u) == static_cast<uint32_t>(n - 1);
+        sync_consumers();
+        if (*last_flag) {
+          int* slot = reinterpret_cast<int*>(scr);                 // n slots
+          float* wt = scr + ((n + 31) / 32) * 32;                  // n x HP weights
+          float* lsum = wt + n * HP;                               // HP sums
+          for (int k = threadIdx.x; k < n; k += W * 32) slot[k] = slot_of(c_lo + k);
+          sync_consumers();
+          for (int hr = warp; hr < rows; hr += W) {  // one warp per row
+            float M = -INFINITY;
+            for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot[k] + hr]).x);
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+            const float ref = exp_ref(M);
+            float ls = 0.f;
+            for (int k = lane; k < n; k += 32) {
+              const float2 ml = __ldcg(&a.part_ml[slot[k] + hr]);
+              const float w = fast_exp2(ml.x - ref);
+              wt[k * HP + hr] = w;
+              ls = fmaf(w, ml.y, ls);
+            }
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, i);
+            if (lane == 0) lsum[hr] = ls;
+          }
+          sync_consumers();
+          for (int i = threadIdx.x; i < quads; i += W * 32) {
+            const int hr = i / (D / 4), d4 = i % (D / 4);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+              const float w = wt[k * HP + hr];
+              const float4 ov = __ldcg(reinterpret_cast<const float4*>(
+                  &a.part_o[static_cast<int64_t>(slot[k] + hr) * D + 4 * d4]));
+              acc.x = fmaf(w, ov.x, acc.x);
+              acc.y = fmaf(w, ov.y, acc.y);
+              acc.z = fmaf(w, ov.z, acc.z);
+              acc.w = fmaf(w, ov.w, acc.w);
+            }
+            write_out(hr, d4, lsum[hr], acc);
+          }
+          if (threadIdx.x == 0) atomicExch(&counters[grp], 0u);
+        }
+      }
+      sync_consumers();  // the scratch is free again
+      ua = ub;
+    }
+  }
+  __syncthreads();
+}
+
+template <int NG, int NT, bool MQ, bool F16>
+int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
+             const CUtensorMap& tmv, cudaStream_t stream) {
+  auto kern = gqa_decode_q4_kernel<NG, NT, MQ, F16>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem_bytes) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(s.grid));
+  cfg.blockDim = dim3(Q4Layout<NG, NT>::kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(s.smem_bytes);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a, s.tiles_per_group, s.passes,
+                         static_cast<int>(s.units), s.stages, a.counters) != cudaSuccess) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
+}
+
+template <int NG, int NT>
+int launch_nt(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
+              const CUtensorMap& tmv, cudaStream_t stream, bool f16) {
+  if (a.Sq > 1)
+    return f16 ? launch_t<NG, NT, true, true>(s, a, tmk, tmv, stream)
+               : launch_t<NG, NT, true, false>(s, a, tmk, tmv, stream);
+  return f16 ? launch_t<NG, NT, false, true>(s, a, tmk, tmv, stream)
+             : launch_t<NG, NT, false, false>(s, a, tmk, tmv, stream);
+}
+
+template <int NG, int NT>
+void fit(DecodeShape& s, int ragged_batch) {
+  for (s.stages = 10;; --s.stages) {
+    s.smem_bytes = Q4Layout<NG, NT>::bytes(s.stages, ragged_batch);
+    if (s.smem_bytes <= kDecodeMaxSmem || s.stages <= 2) break;
+  }
+}
+
+}  // namespace
+
+DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
+  DecodeShape s{};
+  const int64_t rows = p.heads_q / p.heads_kv * p.seq_q;
+  s.D = p.head_dim <= 64 ? 64 : 128;
+  s.NT = rows <= 8 ? 1 : 2;
+  s.HP = 8 * s.NT;
+  s.passes = static_cast<int>((rows + s.HP - 1) / s.HP);
+  s.ragged = p.kv_lens != nullptr;
+  s.tiles_per_group =
+      s.ragged ? static_cast<int>((p.seq_k + KT - 1) / KT)
+               : decode_key_range(p.seq_k, p.seq_k, p.seq_q, p.causal, p.causal_offset, p.window)
+                     .tiles;
+  if (s.tiles_per_group < 1) s.tiles_per_group = 1;
+  s.groups = p.batch * p.heads_kv * s.passes;
+  s.units = s.groups * s.tiles_per_group;
+  s.grid = static_cast<int>(s.units < sm_count ? s.units : sm_count);
+  if (s.grid < 1) s.grid = 1;
+  const int rb = s.ragged ? static_cast<int>(p.batch) : 0;
+  if (s.D == 128)
+    s.NT == 1 ? fit<4, 1>(s, rb) : fit<4, 2>(s, rb);
+  else
+    s.NT == 1 ? fit<2, 1>(s, rb) : fit<2, 2>(s, rb);
+  const int64_t slots = static_cast<int64_t>(s.grid) * 2 * s.HP;
+  int64_t at = kScratchOffset;
+  s.zero_counters = s.groups * 4 > kCounterRegionBytes;
+  s.counters_offset = kWorkspaceHeadBytes;
+  if (s.zero_counters) {
+    s.counters_offset = at;
+    at += ((s.groups * 4 + 255) / 256) * 256;
+  }
+  s.part_ml_offset = at;
+  s.part_o_offset = s.part_ml_offset + ((slots * 8 + 255) / 256) * 256;
+  s.workspace_end = s.part_o_offset + slots * s.D * 4;
+  return s;
+}
+
+int decode_q4_threads(const DecodeShape& s) {
+  return s.NT == 1 ? Q4Layout<4, 1>::kThreads : Q4Layout<4, 2>::kThreads;
+}
+
+int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
+                     const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
+  const bool f16 = p.dtype == GQA_DTYPE_F16;
+  if (s.D == 128)
+    return s.NT == 1 ? launch_nt<4, 1>(s, a, tmk, tmv, stream, f16)
+                     : launch_nt<4, 2>(s, a, tmk, tmv, stream, f16);
+  return s.NT == 1 ? launch_nt<2, 1>(s, a, tmk, tmv, stream, f16)
+                   : launch_nt<2, 2>(s, a, tmk, tmv, stream, f16);
+}
+
+}  // namespace gqa

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,6 +14,7 @@ namespace gqa {
 int validate_problem(const gqa_problem* p);       // sizes, strides, scalars (api.cu)
 bool nothing_visible(const gqa_problem& p);       // causal / window hide every key from every query
 int device_sm_count(int* out);                    // SMs of the current device, or GQA_ERR_DEVICE
+PFN_cuTensorMapEncodeTiled_v12000 get_encoder();  // driver's tensor-map encoder, or nullptr
 
 // ------------------------------------------------------------ decode
 // Keys per streamed tile and consumer warps per CTA of the decode kernel.
@@ -102,7 +104,7 @@ struct DecodeArgs {
   int page_size, num_pages;
   int B, Hq, Hkv, Sk, g;
   int Sq, rows;            // queries per kv head; rows = g * Sq
-  int causal;
+  int causal, has_mask;
   int64_t causal_offset, window;
   float scale_log2;  // scale * log2(e)
   uint64_t* trace;   // per-CTA phase timestamps (kDecodeTraceWords each), or nullptr
@@ -255,9 +257,12 @@ struct Q4RowsArgs {
 int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 
-// Attention over records: one warp per output row.
-int launch_q4_rows(const gqa_problem& p, const void* q, const uint8_t* k, const uint8_t* v,
-                   const uint8_t* mask, void* out, uint32_t* err, cudaStream_t stream);
+// Attention over records for single tokens and short query blocks: the shape,
+// arguments (make_decode_args) and workspace of the 16-bit decode.
+DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
+int decode_q4_threads(const DecodeShape& s);
+int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
+                     const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
 
 // ------------------------------------------------------------ fill: zeros (seq_k == 0) or NaN
 int launch_zero(const gqa_problem& p, void* out, cudaStream_t stream, bool nan);

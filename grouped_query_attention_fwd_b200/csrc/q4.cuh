@@ -17,6 +17,11 @@ constexpr int kHeadBytes = 16;  // scale and minimum of up to four groups
 __host__ __device__ constexpr int groups_of(int D) { return (D + kGroup - 1) / kGroup; }
 __host__ __device__ constexpr int record_bytes(int D) { return kHeadBytes + 16 * groups_of(D); }
 
+template <bool V>
+struct BoolConst {
+  static constexpr bool value = V;
+};
+
 // 16-bit pattern <-> fp32 of the cache's type.
 template <bool F16>
 __device__ __forceinline__ float to_f32(uint32_t bits16) {
