@@ -55,9 +55,11 @@ namespace {
 using namespace q4;
 
 constexpr int KT = kDecodeKeysPerTile;
-constexpr int kChunk = 16;                 // keys a warp takes at a time
+constexpr int kSub = 2;                    // 16-key MMA tiles a warp takes at a time
+constexpr int kChunk = 16 * kSub;          // its keys
 constexpr int kChunks = KT / kChunk;
 constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
+constexpr int kFastMerge = 4;              // split groups merged with all loads in flight
 
 template <int NG, int NT>
 struct Q4Layout {
@@ -70,8 +72,9 @@ struct Q4Layout {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kRow = D + 4;               // a row's O, then (m, l), padded (floats)
   static constexpr int kScratch = W * HP * kRow * 4;
+  static constexpr int kQRows = HP * D * 2;        // Q rows of the range's second group
   static int bytes(int stages, int ragged_batch) {
-    return 128 /*alignment slack*/ + stages * kStage + kScratch + 2 * stages * 8 + 16 +
+    return 128 /*alignment slack*/ + stages * kStage + kScratch + kQRows + 2 * stages * 8 + 16 +
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
 };
@@ -92,6 +95,12 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ void ldmatrix_x2(uint32_t& r0, uint32_t& r1, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];"
+               : "=r"(r0), "=r"(r1)
+               : "r"(addr));
 }
 
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
@@ -144,10 +153,16 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                              ~static_cast<uintptr_t>(127));
   float* scr = reinterpret_cast<float*>(ring + stages * L::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scr) + L::kScratch);
+  uint16_t* q_next = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(scr) + L::kScratch);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(q_next) + L::kQRows);
   uint64_t* empty = full + stages;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + stages);
   volatile int* last_flag = abort_flag + 1;
+  volatile int* fast_flag = abort_flag + 2;  // the final split group is merged here directly
+  // Ticket count of the final split group, read by the producer near the end
+  // of the range (kNoPeek until then).
+  volatile uint32_t* peek_count = reinterpret_cast<volatile uint32_t*>(abort_flag + 3);
+  constexpr uint32_t kNoPeek = 0xFFFFFFFFu;
   int* len_s = reinterpret_cast<int*>(const_cast<int*>(abort_flag) + 4);
   int* pre_s = len_s + a.B;
 
@@ -155,6 +170,8 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   const int lane = threadIdx.x & 31;
   const bool ragged = a.lens != nullptr;
   const int gpb = a.Hkv * passes;
+  auto trace = [&]() { return a.trace + blockIdx.x * kDecodeTraceWords; };  // diagnostics
+  const uint64_t t_entry = (a.trace != nullptr && threadIdx.x == 0) ? globaltimer_ns() : 0;
 
   if (threadIdx.x == W * 32) {
     prefetch_tmap(&tmk);
@@ -166,6 +183,8 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       mbar_init(&empty[s], kChunks);  // one arrival per chunk
     }
     *abort_flag = 0;
+    *fast_flag = 0;
+    *peek_count = kNoPeek;
     fence_mbar_init();
   }
   // From here on global memory written by earlier work on the stream is read.
@@ -182,6 +201,11 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     }
   }
   __syncthreads();
+  if (a.trace != nullptr && threadIdx.x == 0) {
+    for (int w = 0; w < kDecodeTraceWords; ++w) trace()[w] = 0;
+    trace()[kTrEntry] = t_entry;
+    trace()[kTrReady] = globaltimer_ns();
+  }
   if (ragged) {
     if (warp == 0) {
       // pre[b + 1] = sum over entries <= b of (groups per entry) x (tiles of the entry).
@@ -218,50 +242,109 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
 
   if (warp == W) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int it = 0;
-      Cursor cu;
-      for (int u = u_begin; u < u_end; ++u, ++it) {
-        const int s = it % stages;
-        const uint32_t round = static_cast<uint32_t>(it / stages);
-        if (round > 0 &&
-            !mbar_wait(&empty[s], (round & 1u) ^ 1u, abort_flag, a.err, kErrDecodeWait, a.wait_ns))
-          break;
-        if (u == a.withhold_unit) {  // test of the bounded waits, as in the 16-bit decode
-          const uint64_t t0 = globaltimer_ns();
-          while (!*abort_flag && globaltimer_ns() - t0 < 4 * a.wait_ns) {
-          }
-          break;
-        }
-        seek(cu, u, sc, a);
-        const int r = u - cu.beg;
-        const int gi = r / cu.kr.tiles;
-        const int key0 = (r - gi * cu.kr.tiles + cu.kr.t0) * KT;
-        const int kv = gi / passes, b = cu.b;
-        uint8_t* st = ring + s * L::kStage;
-        mbar_arrive_expect_tx(&full[s], L::kStage);
-        if (a.bt != nullptr) {
-          // Two 64-key boxes, each inside one page; one past the sequence's
-          // length takes page num_pages, which TMA fills with zeros.
-          const int len = sc.len ? sc.len[b] : a.Sk;
+    // Group by group of the range, with everything that a unit's copies need
+    // kept in counters: the producer shares its scheduler with consumers, and
+    // a unit has to be on its way every ~800 cycles.  With a paged cache the
+    // units go in blocks of 16: lane i holds the page of half i % 2 (64 keys)
+    // of unit i / 2 of the block, read one block ahead of its use, so that the
+    // table's latency stays off the path of the copies.
+    constexpr int kBlock = 32 / (KT / kDecodePageBox);
+    const bool paged = a.bt != nullptr;
+    int it = 0, s = 0;          // units issued; stage of the next one
+    uint32_t parity = 1;        // of the wait for a free stage (passes at once in round 0)
+    bool ok = true;
+    Cursor cu;
+    for (int ua = u_begin; ua < u_end && ok;) {
+      seek(cu, ua, sc, a);
+      const int gi = (ua - cu.beg) / cu.kr.tiles;
+      const int g_beg = cu.beg + gi * cu.kr.tiles;
+      const int ub = min(u_end, g_beg + cu.kr.tiles);
+      const int kv = gi / passes, b = cu.b;
+      int key0 = (ua - g_beg + cu.kr.t0) * KT;
+      const int len = sc.len ? sc.len[b] : a.Sk;
+      // Page and row of a 64-key box; one past the sequence's length takes
+      // page num_pages, which is out of range: TMA fills it with zeros.
+      auto page_of = [&](int key, bool wanted) {
+        if (!wanted || key >= len) return a.num_pages;
+        const int page = __ldg(a.bt + b * a.bt_stride + key / a.page_size);
+        if (page >= 0 && page < a.num_pages) return page;
+        atomicOr(a.err, kErrPage);
+        return a.num_pages;  // read as zeros
+      };
+      const int at = (lane >> 1) * KT + (lane & 1) * kDecodePageBox;
+      int next_page = paged ? page_of(key0 + at, ua + (lane >> 1) < ub) : 0;
+      for (int u = ua; u < ub && ok;) {
+        const int my_page = next_page;
+        const int my_row = paged ? (key0 + at) % a.page_size : 0;
+        const int u_stop = min(u + kBlock, ub);
+        if (paged) next_page = page_of(key0 + kBlock * KT + at, u + kBlock + (lane >> 1) < ub);
+        for (int i = 0; u < u_stop; ++u, ++i, key0 += KT) {
+          int page[2] = {0, 0}, row[2] = {0, 0};
+          if (paged) {
 #pragma unroll
-          for (int h = 0; h < KT / kDecodePageBox; ++h) {
-            const int key = key0 + h * kDecodePageBox;
-            int page = a.num_pages;
-            if (key < len) {
-              page = __ldg(a.bt + b * a.bt_stride + key / a.page_size);
-              if (page < 0 || page >= a.num_pages) {
-                atomicOr(a.err, kErrPage);
-                page = a.num_pages;  // read as zeros
-              }
+            for (int h = 0; h < 2; ++h) {
+              page[h] = __shfl_sync(0xffffffffu, my_page, 2 * i + h);
+              row[h] = __shfl_sync(0xffffffffu, my_row, 2 * i + h);
             }
-            uint8_t* dst = st + h * kDecodePageBox * P;
-            tma_load_4d(dst, &tmk, &full[s], 0, key % a.page_size, kv, page);
-            tma_load_4d(dst + L::kTile, &tmv, &full[s], 0, key % a.page_size, kv, page);
           }
-        } else {
-          tma_load_4d(st, &tmk, &full[s], 0, key0, kv, b);
-          tma_load_4d(st + L::kTile, &tmv, &full[s], 0, key0, kv, b);
+          // (Every lane waits: the warp stays converged.)
+          ok = __all_sync(0xffffffffu, mbar_try_wait(&empty[s], parity) ||
+                                           mbar_wait(&empty[s], parity, abort_flag, a.err,
+                                                     kErrDecodeWait, a.wait_ns));
+          if (ok && u == a.withhold_unit) {
+            // Test of the bounded waits, as in the 16-bit decode: nothing more
+            // is issued, and the consumers' wait for this unit runs out.
+            const uint64_t t0 = globaltimer_ns();
+            while (!*abort_flag && globaltimer_ns() - t0 < 4 * a.wait_ns) {
+            }
+            __syncwarp();
+            ok = false;
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            uint8_t* st = ring + s * L::kStage;
+            mbar_arrive_expect_tx(&full[s], L::kStage);
+            if (paged) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint8_t* dst = st + h * kDecodePageBox * P;
+                tma_load_4d(dst, &tmk, &full[s], 0, row[h], kv, page[h]);
+                tma_load_4d(dst + L::kTile, &tmv, &full[s], 0, row[h], kv, page[h]);
+              }
+            } else {
+              tma_load_4d(st, &tmk, &full[s], 0, key0, kv, b);
+              tma_load_4d(st + L::kTile, &tmv, &full[s], 0, key0, kv, b);
+            }
+            if (a.trace != nullptr && it == 0) trace()[kTrFirstIssue] = globaltimer_ns();
+          }
+          __syncwarp();
+          ++it;
+          if (++s == stages) {
+            s = 0;
+            parity ^= 1u;
+          }
+        }
+      }
+      ua = ub;
+    }
+    if (lane == 0) {
+      if (a.trace != nullptr) trace()[kTrLastIssue] = globaltimer_ns();
+      // Final group split over several CTAs: once the consumers are on the
+      // range's last unit, read its ticket count for their final merge (the
+      // fence makes the partials published before those tickets visible).
+      if (!*abort_flag && u_begin < u_end) {
+        seek(cu, u_end - 1, sc, a);
+        const int gi = (u_end - 1 - cu.beg) / cu.kr.tiles;
+        const int g_beg = cu.beg + gi * cu.kr.tiles;
+        if (cta_of_unit(g_beg, sc.total, sc.P) !=
+            cta_of_unit(g_beg + cu.kr.tiles - 1, sc.total, sc.P)) {
+          const int j = it - 2;  // second-to-last unit of the range
+          if (j < 0 || mbar_wait(&empty[j % stages], static_cast<uint32_t>((j / stages) & 1),
+                                 abort_flag, a.err, kErrDecodeWait, a.wait_ns)) {
+            const uint32_t n = ld_relaxed_gpu(&counters[cu.b * gpb + gi]);
+            fence_acq_rel_gpu();
+            *peek_count = n;
+          }
         }
       }
       // Unwind: no copy may still be landing in this CTA's shared memory.
@@ -275,36 +358,147 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     const int c = lane & 3, r8 = lane >> 2;
     auto sync_consumers = [] { asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory"); };
     Cursor cu;
+    // Address of row hl (a head, or a (head, query) pair) of kv head kv of entry b.
+    auto q_row = [&](int b, int kv, int hl) {
+      const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
+      return a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
+             static_cast<int64_t>(qi) * a.qs[2];
+    };
+    int mid_ticket = -1;  // thread 0: the first group's ticket, taken before the range's end
+    // Group of a unit: its place in the launch, and who shares it.
+    struct Group {
+      int b, kv, pass, id, beg, tiles, c_lo, c_hi, rows;
+    };
+    auto group_at = [&](int u) {
+      seek(cu, u, sc, a);
+      const int gi = (u - cu.beg) / cu.kr.tiles;
+      Group g;
+      g.b = cu.b;
+      g.kv = gi / passes;
+      g.pass = gi % passes;
+      g.id = cu.b * gpb + gi;
+      g.beg = cu.beg + gi * cu.kr.tiles;
+      g.tiles = cu.kr.tiles;
+      g.c_lo = cta_of_unit(g.beg, sc.total, sc.P);
+      g.c_hi = cta_of_unit(g.beg + g.tiles - 1, sc.total, sc.P);
+      g.rows = min(HP, a.rows - g.pass * HP);
+      return g;
+    };
+    // Output row hr of a group's pass, dims 4 d4 .. + 3.
+    auto write_out = [&](const Group& g, int hr, int d4, float lsum, const float4& acc) {
+      if (4 * d4 >= a.Dv) return;
+      const int row = g.pass * HP + hr;
+      const int hh = MQ ? row / a.Sq : row, qi = MQ ? row % a.Sq : 0;
+      const float inv = 1.f / lsum;  // no visible key: 0 * inf = NaN
+      uint2 pk;
+      pk.x = pack2<F16>(acc.x * inv, acc.y * inv);
+      pk.y = pack2<F16>(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(a.out + g.b * a.os[0] +
+                                static_cast<int64_t>(g.kv * a.g + hh) * a.os[1] +
+                                static_cast<int64_t>(qi) * a.os[2] + 4 * d4) = pk;
+    };
+    // Partial slot of a CTA for a split group: only a range's first and last
+    // group can be split, so there are two.
+    auto slot_of = [&](int cta, int id) {
+      const int first = group_of(range_start(cta, sc.total, sc.P), sc, a);
+      return (cta * 2 + (first == id ? 0 : 1)) * HP;
+    };
+    // All partials of a split group are published: their merge, by the whole
+    // consumer group, through the scratch.
+    auto merge_partials = [&](const Group& g) {
+      const int n = g.c_hi - g.c_lo + 1;
+      int* slot = reinterpret_cast<int*>(scr);  // n slots
+      float* wt = scr + ((n + 31) / 32) * 32;   // n x HP weights
+      float* lsum = wt + n * HP;                // HP sums
+      for (int k = threadIdx.x; k < n; k += W * 32) slot[k] = slot_of(g.c_lo + k, g.id);
+      sync_consumers();
+      for (int hr = warp; hr < g.rows; hr += W) {  // one warp per row
+        float M = -INFINITY;
+        for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot[k] + hr]).x);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
+        const float ref = exp_ref(M);
+        float ls = 0.f;
+        for (int k = lane; k < n; k += 32) {
+          const float2 ml = __ldcg(&a.part_ml[slot[k] + hr]);
+          const float w = fast_exp2(ml.x - ref);
+          wt[k * HP + hr] = w;
+          ls = fmaf(w, ml.y, ls);
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, i);
+        if (lane == 0) lsum[hr] = ls;
+      }
+      sync_consumers();
+      for (int i = threadIdx.x; i < g.rows * (D / 4); i += W * 32) {
+        const int hr = i / (D / 4), d4 = i % (D / 4);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+          const float w = wt[k * HP + hr];
+          const float4 ov = __ldcg(reinterpret_cast<const float4*>(
+              &a.part_o[static_cast<int64_t>(slot[k] + hr) * D + 4 * d4]));
+          acc.x = fmaf(w, ov.x, acc.x);
+          acc.y = fmaf(w, ov.y, acc.y);
+          acc.z = fmaf(w, ov.z, acc.z);
+          acc.w = fmaf(w, ov.w, acc.w);
+        }
+        write_out(g, hr, d4, lsum[hr], acc);
+      }
+      if (threadIdx.x == 0) atomicExch(&counters[g.id], 0u);
+      sync_consumers();
+    };
+
+    // The Q rows of the range's second group are fetched now: at the change
+    // of groups they would cost a round trip.  (The first group's come while
+    // its first unit does; a range over more groups has short ones, and
+    // fetches the others' when it gets there.)
+    int u_second = u_end;
+    if (u_begin < u_end) {
+      const Group g0 = group_at(u_begin);
+      u_second = g0.beg + g0.tiles;
+      if (u_second < u_end) {
+        const Group g1 = group_at(u_second);
+        for (int i = threadIdx.x; i < HP * (D / 8); i += W * 32) {
+          const int hr = i / (D / 8), d8 = i % (D / 8);
+          uint16_t* dst = q_next + i * 8;
+          if (hr < g1.rows && d8 * 8 < a.Dv)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
+                         "l"(q_row(g1.b, g1.kv, g1.pass * HP + hr) + d8 * 8)
+                         : "memory");
+          else
+            *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+    }
+
     for (int ua = u_begin; ua < u_end;) {
       // One group (kv head and pass of one entry): units [ua, ub) of this range.
-      seek(cu, ua, sc, a);
-      const int gi = (ua - cu.beg) / cu.kr.tiles;
-      const int grp_beg = cu.beg + gi * cu.kr.tiles;
-      const int grp_tiles = cu.kr.tiles;
-      const int ub = min(u_end, grp_beg + grp_tiles);
-      const int tile0 = ua - grp_beg + cu.kr.t0;
-      const int kv = gi / passes, pass = gi % passes, b = cu.b;
+      const Group grp = group_at(ua);
+      const int ub = min(u_end, grp.beg + grp.tiles);
+      const int tile0 = ua - grp.beg + cu.kr.t0;
+      const int kv = grp.kv, pass = grp.pass, b = grp.b;
       const int len = sc.len ? sc.len[b] : a.Sk;
-      const int grp = b * gpb + gi;
 
       // Q as B fragments, thread (r8, c): row r8 of each column tile, dims
-      // 32 t + 8 c .. + 7; sums over each group's dims for the minima.
-      uint32_t bq[NT][NG][4];
-      float qs[NT][NG][2], fac[NT][2];
+      // 32 t + 8 c .. + 7; and the sums over each group's dims, the factors
+      // of the minima, as two 16-bit parts: a record's head is the A operand
+      // of a product of its own, and its scales meet zeros.
+      uint32_t bq[NT][NG][4], bm[NT][2];
+      float fac[NT][2];
       int vlo[NT][2], vhi[NT][2];          // visible keys of this thread's two rows (MQ)
       const uint8_t* vmask[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int hl = pass * HP + nt * 8 + r8;
-        const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
-        const uint16_t* qrow = a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
-                               static_cast<int64_t>(qi) * a.qs[2];
+        const bool stashed = ua == u_second;
+        const uint16_t* qrow = stashed ? q_next + (nt * 8 + r8) * D : q_row(b, kv, hl);
         float f[NG][8];
         float amax = 0.f;
 #pragma unroll
         for (int t = 0; t < NG; ++t) {
           uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (hl < a.rows && 32 * t + 8 * c < a.Dv)
+          if (stashed || (hl < a.rows && 32 * t + 8 * c < a.Dv))
             x = *reinterpret_cast<const uint4*>(qrow + 32 * t + 8 * c);
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -328,7 +522,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           up = 0x1p64f;
           back = 0x1p69f;
         }
-        float sums[NG];
+        float mine = 0.f;  // group c's sum
 #pragma unroll
         for (int t = 0; t < NG; ++t) {
           float s = 0.f;
@@ -336,18 +530,19 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           for (int i = 0; i < 8; ++i) s += f[t][i];
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
-          sums[t] = s / back;  // a power of two: exact
+          if (t == c) mine = s / back;  // a power of two: exact
           const float odd = up * 0.0625f;
           bq[nt][t][0] = pack2<F16>(f[t][0] * up, f[t][4] * up);
           bq[nt][t][1] = pack2<F16>(f[t][1] * odd, f[t][5] * odd);
           bq[nt][t][2] = pack2<F16>(f[t][2] * up, f[t][6] * up);
           bq[nt][t][3] = pack2<F16>(f[t][3] * odd, f[t][7] * odd);
         }
+        const uint32_t high = to_16<F16>(mine);
+        bm[nt][0] = high << 16;
+        bm[nt][1] = to_16<F16>(mine - to_f32<F16>(high)) << 16;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int src = (2 * c + e) * 4;
-#pragma unroll
-          for (int t = 0; t < NG; ++t) qs[nt][t][e] = __shfl_sync(0xffffffffu, sums[t], src);
           fac[nt][e] = a.scale_log2 * __shfl_sync(0xffffffffu, back, src);
           const int row = pass * HP + nt * 8 + 2 * c + e;
           const int i = MQ ? (row < a.rows ? row : 0) % a.Sq : 0;
@@ -380,13 +575,15 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       }
 
       float o[NT][NG][2][4], corr[NT][NG][2];
-      float m_ref[NT][2], l[NT][2];
+      // The exponent reference (running maximum), its negative with 0 for
+      // -inf, and the score above which it moves.
+      float m_ref[NT][2], m_neg[NT][2], m_top[NT][2], l[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m_ref[nt][e] = -INFINITY;
-          l[nt][e] = 0.f;
+          m_ref[nt][e] = m_top[nt][e] = -INFINITY;
+          m_neg[nt][e] = l[nt][e] = 0.f;
 #pragma unroll
           for (int t = 0; t < NG; ++t) {
             corr[nt][t][e] = 0.f;
@@ -410,95 +607,105 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         const int chunk = x % kChunks;
         const int key0 = (tile0 + it - (ua - u_begin)) * KT + chunk * kChunk;
         const bool landed =
+            mbar_try_wait(&full[s], parity) ||
             mbar_wait(&full[s], parity, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
+        if (a.trace != nullptr && x == 0 && lane == 0) trace()[kTrFirstLand] = globaltimer_ns();
         // (A wait that gave up sets the abort flag: the arithmetic is skipped,
         // the walk goes on, so that all warps reach the same barriers.)
-        const bool work = landed && key0 < cu.kr.hi && key0 + kChunk > cu.kr.lo;
-        if (!__any_sync(0xffffffffu, work)) {
+        if (!__all_sync(0xffffffffu, landed) || key0 >= cu.kr.hi || key0 + kChunk <= cu.kr.lo) {
           if (lane == 0) mbar_arrive(&empty[s]);
           continue;
         }
         const uint32_t kb = smem_u32(ring + s * L::kStage) + chunk * kChunk * P;
         const uint32_t vb = kb + L::kTile;
-        // Codes and parameters of the chunk's 16 records, K and V.
-        const uint32_t row_at = ((lane >> 3) & 1) * 8 + (lane & 7);
-        const uint32_t at = row_at * P + kHeadBytes + (lane >> 4) * 16;
-        uint32_t kw[NG][2], vw[NG][2];  // [group][keys 0-7 | 8-15]
-#pragma unroll
-        for (int t = 0; t < NG; t += 2)
-          ldmatrix_x4(kw[t][0], kw[t][1], kw[t + 1][0], kw[t + 1][1], kb + at + t * 16);
-        uint32_t kp[2][NG], vp[2][NG];  // [key r8 | r8 + 8][group]
-        load_params<NG>(kp[0], kb + r8 * P);
-        load_params<NG>(kp[1], kb + (r8 + 8) * P);
-#pragma unroll
-        for (int t = 0; t < NG; t += 2)
-          ldmatrix_x4_trans(vw[t][0], vw[t][1], vw[t + 1][0], vw[t + 1][1], vb + at + t * 16);
-        load_params<NG>(vp[0], vb + r8 * P);
-        load_params<NG>(vp[1], vb + (r8 + 8) * P);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);  // the chunk is in registers
+        // ldmatrix row of this lane: 8-key halves, then groups.
+        const uint32_t at =
+            (((lane >> 3) & 1) * 8 + (lane & 7)) * P + kHeadBytes + (lane >> 4) * 16;
 
-        float sv[NT][4];  // scores: keys r8 (0, 1) and r8 + 8 (2, 3), rows 2 c + {0, 1}
+        float sv[kSub][NT][4];  // scores: keys r8 (0, 1) and r8 + 8 (2, 3), rows 2 c + {0, 1}
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < kSub; ++j) {
+          const uint32_t kj = kb + j * 16 * P;
+          uint32_t kw[NG][2], kp[2][NG], h0, h1;  // codes [group][key half], heads
 #pragma unroll
-          for (int y = 0; y < 4; ++y) sv[nt][y] = 0.f;
+          for (int t = 0; t < NG; t += 2)
+            ldmatrix_x4(kw[t][0], kw[t][1], kw[t + 1][0], kw[t + 1][1], kj + at + t * 16);
+          ldmatrix_x2(h0, h1, kj + (lane & 15) * P);
+          load_params<NG>(kp[0], kj + r8 * P);
+          load_params<NG>(kp[1], kj + (r8 + 8) * P);
 #pragma unroll
-        for (int t = 0; t < NG; ++t) {
-          const uint32_t a8 = kw[t][0] >> 8, b8 = kw[t][1] >> 8;
+          for (int nt = 0; nt < NT; ++nt)
+            mma_zero<F16>(sv[j][nt], h0, h1, h0, h1, bm[nt][0], bm[nt][1]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            mma_zero<F16>(acc, kw[t][0] & 0x000F000Fu, kw[t][1] & 0x000F000Fu,
-                          kw[t][0] & 0x00F000F0u, kw[t][1] & 0x00F000F0u, bq[nt][t][0],
-                          bq[nt][t][1]);
-            mma_16816<F16>(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
-                           b8 & 0x00F000F0u, bq[nt][t][2], bq[nt][t][3]);
+          for (int t = 0; t < NG; ++t) {
+            const uint32_t a8 = kw[t][0] >> 8, b8 = kw[t][1] >> 8;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              sv[nt][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y],
-                               fmaf(min_of<F16>(kp[y >> 1][t]), qs[nt][t][y & 1], sv[nt][y]));
+            for (int nt = 0; nt < NT; ++nt) {
+              float acc[4];
+              mma_zero<F16>(acc, kw[t][0] & 0x000F000Fu, kw[t][1] & 0x000F000Fu,
+                            kw[t][0] & 0x00F000F0u, kw[t][1] & 0x00F000F0u, bq[nt][t][0],
+                            bq[nt][t][1]);
+              mma_16816<F16>(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                             b8 & 0x00F000F0u, bq[nt][t][2], bq[nt][t][3]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                sv[j][nt][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y], sv[j][nt][y]);
+            }
           }
         }
         // log2 of each key's largest V scale (see the top), within 2^-60 .. 2^100.
-        float lsv[2];
+        float lsv[kSub][2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float m = 0x1p-60f;
+        for (int j = 0; j < kSub; ++j)
 #pragma unroll
-          for (int t = 0; t < NG; ++t) m = fmaxf(m, scale_of<F16>(vp[k][t]));
-          lsv[k] = fast_lg2(fminf(m, 0x1p100f));
-        }
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[NG];
+            load_params<NG>(w, vb + (j * 16 + k * 8 + r8) * P);
+            float m = 0x1p-60f;
+#pragma unroll
+            for (int t = 0; t < NG; t += 2)
+              m = fmax3(m, scale_of<F16>(w[t]), scale_of<F16>(w[t + 1]));
+            lsv[j][k] = fast_lg2(fminf(m, 0x1p100f));
+          }
 
         auto rest = [&](auto whole) {
           constexpr bool kWhole = decltype(whole)::value;
-          // Scores in base 2; hidden keys -inf.
+          // Scores in base 2 are sv * fac; with hidden keys the product is
+          // taken first and replaced by -inf.
           bool raise = false;
-          bool seen[NT][4];
+          bool seen[kSub][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < kSub; ++j)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int e = y & 1, key = key0 + r8 + (y >> 1) * 8;
-              float t = sv[nt][y] * fac[nt][e];
-              seen[nt][y] = kWhole || (key >= vlo[nt][e] && key < vhi[nt][e] &&
-                                       mask_allows(vmask[nt][e], key));
-              if (!seen[nt][y]) t = -INFINITY;
-              sv[nt][y] = t;
-              raise |= t + lsv[y >> 1] > m_ref[nt][e] + kLazyLog2;
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int e = y & 1, key = key0 + j * 16 + r8 + (y >> 1) * 8;
+                float& t = sv[j][nt][y];
+                seen[j][nt][y] = kWhole || (key >= vlo[nt][e] && key < vhi[nt][e] &&
+                                            mask_allows(vmask[nt][e], key));
+                if (!kWhole) t = seen[j][nt][y] ? t * fac[nt][e] : -INFINITY;
+                raise |= fmaf(t, kWhole ? fac[nt][e] : 1.f, lsv[j][y >> 1]) > m_top[nt][e];
+              }
           if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(sv[nt][e] + lsv[0], sv[nt][2 + e] + lsv[1]);
+                const float f = kWhole ? fac[nt][e] : 1.f;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kSub; ++j)
+                  mx = fmax3(mx, fmaf(sv[j][nt][e], f, lsv[j][0]),
+                             fmaf(sv[j][nt][2 + e], f, lsv[j][1]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 const float m_new = fmaxf(m_ref[nt][e], mx);
-                const float alpha = fast_exp2(m_ref[nt][e] - exp_ref(m_new));
+                m_neg[nt][e] = -exp_ref(m_new);
+                const float alpha = fast_exp2(m_ref[nt][e] + m_neg[nt][e]);
                 m_ref[nt][e] = m_new;
+                m_top[nt][e] = m_new + kLazyLog2;
                 l[nt][e] *= alpha;
 #pragma unroll
                 for (int t = 0; t < NG; ++t) {
@@ -512,44 +719,60 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
               }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+          for (int j = 0; j < kSub; ++j) {
+            uint32_t vw[NG][2], vp[2][NG];
+            load_params<NG>(vp[0], vb + (j * 16 + r8) * P);
+            load_params<NG>(vp[1], vb + (j * 16 + 8 + r8) * P);
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              sv[nt][y] = fast_exp2(sv[nt][y] - exp_ref(m_ref[nt][y & 1]));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) l[nt][e] += sv[nt][e] + sv[nt][2 + e];
-          }
-#pragma unroll
-          for (int t = 0; t < NG; ++t) {
-            const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const float scale = scale_of<F16>(vp[k][t]);
-                float add = min_of<F16>(vp[k][t]);
-                if (F16) add = fmaf(8.f, scale, add);
-                float w0 = sv[nt][2 * k] * scale, w1 = sv[nt][2 * k + 1] * scale;
-                float c0 = sv[nt][2 * k] * add, c1 = sv[nt][2 * k + 1] * add;
-                if (!kWhole) {  // a hidden key's parameters may be NaN
-                  w0 = seen[nt][2 * k] ? w0 : 0.f;
-                  w1 = seen[nt][2 * k + 1] ? w1 : 0.f;
-                  c0 = seen[nt][2 * k] ? c0 : 0.f;
-                  c1 = seen[nt][2 * k + 1] ? c1 : 0.f;
-                }
-                corr[nt][t][0] += c0;
-                corr[nt][t][1] += c1;
-                pb[nt][k] = movmatrix_trans(pack_f16x2(w0, w1));
-              }
-            const uint32_t x0 = v_codes_lo<F16>(vw[t][0]), x1 = v_codes_hi<F16>(vw[t][0]);
-            const uint32_t x2 = v_codes_lo<F16>(vw[t][1]), x3 = v_codes_hi<F16>(vw[t][1]);
-            const uint32_t y0 = v_codes_lo<F16>(v0), y1 = v_codes_hi<F16>(v0);
-            const uint32_t y2 = v_codes_lo<F16>(v1), y3 = v_codes_hi<F16>(v1);
+            for (int t = 0; t < NG; t += 2)
+              ldmatrix_x4_trans(vw[t][0], vw[t][1], vw[t + 1][0], vw[t + 1][1],
+                                vb + j * 16 * P + at + t * 16);
+            if (j == kSub - 1) {  // all of the chunk is in registers
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&empty[s]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(o[nt][t][0], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
-              mma_f16_16816(o[nt][t][1], y0, y1, y2, y3, pb[nt][0], pb[nt][1]);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                sv[j][nt][y] = fast_exp2(fmaf(sv[j][nt][y], kWhole ? fac[nt][y & 1] : 1.f,
+                                              m_neg[nt][y & 1]));
+#pragma unroll
+              for (int e = 0; e < 2; ++e) l[nt][e] += sv[j][nt][e] + sv[j][nt][2 + e];
+            }
+#pragma unroll
+            for (int t = 0; t < NG; ++t) {
+              const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
+              uint32_t pb[NT][2];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float scale = scale_of<F16>(vp[k][t]);
+                  float add = min_of<F16>(vp[k][t]);
+                  if (F16) add = fmaf(8.f, scale, add);
+                  const float p0 = sv[j][nt][2 * k], p1 = sv[j][nt][2 * k + 1];
+                  float w0 = p0 * scale, w1 = p1 * scale;
+                  if (kWhole) {
+                    corr[nt][t][0] = fmaf(p0, add, corr[nt][t][0]);
+                    corr[nt][t][1] = fmaf(p1, add, corr[nt][t][1]);
+                  } else {  // a hidden key's parameters may be NaN
+                    w0 = seen[j][nt][2 * k] ? w0 : 0.f;
+                    w1 = seen[j][nt][2 * k + 1] ? w1 : 0.f;
+                    corr[nt][t][0] += seen[j][nt][2 * k] ? p0 * add : 0.f;
+                    corr[nt][t][1] += seen[j][nt][2 * k + 1] ? p1 * add : 0.f;
+                  }
+                  pb[nt][k] = movmatrix_trans(pack_f16x2(w0, w1));
+                }
+              const uint32_t x0 = v_codes_lo<F16>(vw[t][0]), x1 = v_codes_hi<F16>(vw[t][0]);
+              const uint32_t x2 = v_codes_lo<F16>(vw[t][1]), x3 = v_codes_hi<F16>(vw[t][1]);
+              const uint32_t y0 = v_codes_lo<F16>(v0), y1 = v_codes_hi<F16>(v0);
+              const uint32_t y2 = v_codes_lo<F16>(v1), y3 = v_codes_hi<F16>(v1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16_16816(o[nt][t][0], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
+                mma_f16_16816(o[nt][t][1], y0, y1, y2, y3, pb[nt][0], pb[nt][1]);
+              }
             }
           }
         };
@@ -560,6 +783,24 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       }
 
       // ---- end of the group: the W warps' states meet in shared memory.
+      if (a.trace != nullptr && threadIdx.x == 0 && ub == u_end) trace()[kTrLastTile] = globaltimer_ns();
+      const bool final_group = ub == u_end;
+      const int n_contrib = grp.c_hi - grp.c_lo + 1;
+      if (final_group && threadIdx.x == 0) {
+        // The other contributors of the range's last group have mostly
+        // published long ago (it was the first of their range); the producer
+        // read the tickets and fenced at gpu scope, and acquiring its store
+        // at CTA scope orders the loads of the partials after theirs.
+        int fast = 0;
+        if (n_contrib > 1 && n_contrib <= kFastMerge &&
+            *peek_count == static_cast<uint32_t>(n_contrib - 1)) {
+          fence_acq_rel_cta();
+          fast = 1;
+        }
+        *fast_flag = fast;
+      }
+      if (ua != u_begin) sync_consumers();  // the last group's states have been read
+      asm volatile("cp.async.wait_all;" ::: "memory");  // (visible to all after the barrier)
       float* mine = scr + warp * HP * R;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -584,8 +825,11 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           if (r8 == 0) *reinterpret_cast<float2*>(mine + h * R + D) = make_float2(m_ref[nt][e], lv);
         }
       sync_consumers();
-      const int rows = min(HP, a.rows - pass * HP);
-      const int quads = rows * (D / 4);
+      if (a.trace != nullptr && threadIdx.x == 0) {
+        trace()[kTrFlushes] += 1;
+        if (final_group) trace()[kTrFinalMerged] = globaltimer_ns();
+      }
+      const int quads = grp.rows * (D / 4);
       // Row hr of the pass, dims 4 d4 .. + 3 over the W states: (M, l, O).
       auto merge_warps = [&](int hr, int d4, float& M, float& lsum, float4& acc) {
         M = -INFINITY;
@@ -606,36 +850,58 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           acc.w = fmaf(wt, ov.w, acc.w);
         }
       };
-      auto write_out = [&](int hr, int d4, float lsum, const float4& acc) {
-        if (4 * d4 >= a.Dv) return;
-        const int row = pass * HP + hr;
-        const int hh = MQ ? row / a.Sq : row, qi = MQ ? row % a.Sq : 0;
-        const float inv = 1.f / lsum;  // no visible key: 0 * inf = NaN
-        uint2 pk;
-        pk.x = pack2<F16>(acc.x * inv, acc.y * inv);
-        pk.y = pack2<F16>(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(a.out + b * a.os[0] +
-                                  static_cast<int64_t>(kv * a.g + hh) * a.os[1] +
-                                  static_cast<int64_t>(qi) * a.os[2] + 4 * d4) = pk;
-      };
-      const int c_lo = cta_of_unit(grp_beg, sc.total, sc.P);
-      const int c_hi = cta_of_unit(grp_beg + grp_tiles - 1, sc.total, sc.P);
-      if (c_lo == c_hi) {
+      if (n_contrib == 1) {
         for (int i = threadIdx.x; i < quads; i += W * 32) {
           float M, lsum;
           float4 acc;
           merge_warps(i / (D / 4), i % (D / 4), M, lsum, acc);
-          write_out(i / (D / 4), i % (D / 4), lsum, acc);
+          write_out(grp, i / (D / 4), i % (D / 4), lsum, acc);
         }
+      } else if (final_group && *fast_flag) {
+        // Every other partial is published: merge them with these states.
+        for (int i = threadIdx.x; i < quads; i += W * 32) {
+          const int hr = i / (D / 4), d4 = i % (D / 4);
+          float2 ml[kFastMerge];
+          float4 ov[kFastMerge];
+#pragma unroll
+          for (int k = 0; k < kFastMerge; ++k) {
+            const int cta = grp.c_lo + k;
+            ml[k] = make_float2(-INFINITY, 0.f);
+            ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < n_contrib && cta != static_cast<int>(blockIdx.x)) {
+              const int64_t at = slot_of(cta, grp.id) + hr;
+              ml[k] = __ldcg(&a.part_ml[at]);
+              ov[k] = __ldcg(reinterpret_cast<const float4*>(&a.part_o[at * D + 4 * d4]));
+            }
+          }
+          float M, lsum;
+          float4 acc;
+          merge_warps(hr, d4, M, lsum, acc);
+          float top = M;
+#pragma unroll
+          for (int k = 0; k < kFastMerge; ++k) top = fmaxf(top, ml[k].x);
+          const float ref = exp_ref(top), own = fast_exp2(M - ref);
+          lsum *= own;
+          acc.x *= own;
+          acc.y *= own;
+          acc.z *= own;
+          acc.w *= own;
+#pragma unroll
+          for (int k = 0; k < kFastMerge; ++k) {
+            const float w = fast_exp2(ml[k].x - ref);
+            lsum = fmaf(w, ml[k].y, lsum);
+            acc.x = fmaf(w, ov[k].x, acc.x);
+            acc.y = fmaf(w, ov[k].y, acc.y);
+            acc.z = fmaf(w, ov[k].z, acc.z);
+            acc.w = fmaf(w, ov[k].w, acc.w);
+          }
+          write_out(grp, hr, d4, lsum, acc);
+        }
+        // All have arrived: the counter goes back to zero for the next launch.
+        if (threadIdx.x == 0) counters[grp.id] = 0u;
       } else {
-        // Split over several CTAs: publish a partial, take a ticket; the last
-        // of them merges.  Only a range's first and last group can be split:
-        // two partial slots per CTA.
-        auto slot_of = [&](int cta) {
-          const int first = group_of(range_start(cta, sc.total, sc.P), sc, a);
-          return (cta * 2 + (first == grp ? 0 : 1)) * HP;
-        };
-        const int base = slot_of(blockIdx.x);
+        // Publish a partial and take a ticket.
+        const int base = slot_of(blockIdx.x, grp.id);
         for (int i = threadIdx.x; i < quads; i += W * 32) {
           const int hr = i / (D / 4), d4 = i % (D / 4);
           float M, lsum;
@@ -644,58 +910,52 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           *reinterpret_cast<float4*>(&a.part_o[static_cast<int64_t>(base + hr) * D + 4 * d4]) = acc;
           if (d4 == 0) a.part_ml[base + hr] = make_float2(M, lsum);
         }
-        sync_consumers();
-        const int n = c_hi - c_lo + 1;
-        if (threadIdx.x == 0)
-          *last_flag = atom_add_acq_rel_gpu(&counters[grp], 1u) == static_cast<uint32_t>(n - 1);
-        sync_consumers();
-        if (*last_flag) {
-          int* slot = reinterpret_cast<int*>(scr);                 // n slots
-          float* wt = scr + ((n + 31) / 32) * 32;                  // n x HP weights
-          float* lsum = wt + n * HP;                               // HP sums
-          for (int k = threadIdx.x; k < n; k += W * 32) slot[k] = slot_of(c_lo + k);
-          sync_consumers();
-          for (int hr = warp; hr < rows; hr += W) {  // one warp per row
-            float M = -INFINITY;
-            for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot[k] + hr]).x);
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-            const float ref = exp_ref(M);
-            float ls = 0.f;
-            for (int k = lane; k < n; k += 32) {
-              const float2 ml = __ldcg(&a.part_ml[slot[k] + hr]);
-              const float w = fast_exp2(ml.x - ref);
-              wt[k * HP + hr] = w;
-              ls = fmaf(w, ml.y, ls);
-            }
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, i);
-            if (lane == 0) lsum[hr] = ls;
+        if (!final_group) {
+          // The range goes on: only warp 0 waits for the others' stores, and
+          // whether this was the group's last ticket is looked at at the end.
+          if (warp == 0) {
+            asm volatile("bar.sync 2, %0;" ::"n"(W * 32) : "memory");
+            if (lane == 0)
+              mid_ticket = static_cast<int>(atom_add_acq_rel_gpu(&counters[grp.id], 1u));
+          } else {
+            asm volatile("bar.arrive 2, %0;" ::"n"(W * 32) : "memory");
           }
+        } else {
+          // (The barrier makes every thread's partial visible to thread 0; its
+          // acquire-release add publishes them and, for the last arriver,
+          // makes the others' visible.)
           sync_consumers();
-          for (int i = threadIdx.x; i < quads; i += W * 32) {
-            const int hr = i / (D / 4), d4 = i % (D / 4);
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-              const float w = wt[k * HP + hr];
-              const float4 ov = __ldcg(reinterpret_cast<const float4*>(
-                  &a.part_o[static_cast<int64_t>(slot[k] + hr) * D + 4 * d4]));
-              acc.x = fmaf(w, ov.x, acc.x);
-              acc.y = fmaf(w, ov.y, acc.y);
-              acc.z = fmaf(w, ov.z, acc.z);
-              acc.w = fmaf(w, ov.w, acc.w);
-            }
-            write_out(hr, d4, lsum[hr], acc);
-          }
-          if (threadIdx.x == 0) atomicExch(&counters[grp], 0u);
+          if (threadIdx.x == 0)
+            *last_flag = atom_add_acq_rel_gpu(&counters[grp.id], 1u) ==
+                         static_cast<uint32_t>(n_contrib - 1);
+          sync_consumers();
+          if (*last_flag) merge_partials(grp);
         }
       }
-      sync_consumers();  // the scratch is free again
+      if (a.trace != nullptr && threadIdx.x == 0 && final_group) {
+        trace()[kTrFinalDone] = globaltimer_ns();
+        trace()[kTrFinalKind] = n_contrib == 1 ? 0 : (*fast_flag ? 2 : 1);
+      }
       ua = ub;
+    }
+    // The first group, where it ended before the range did and this CTA was
+    // the last of its contributors.
+    if (u_second < u_end) {
+      const Group g0 = group_at(u_begin);
+      if (g0.c_lo != g0.c_hi) {
+        sync_consumers();
+        if (threadIdx.x == 0) *last_flag = mid_ticket == g0.c_hi - g0.c_lo;
+        sync_consumers();
+        if (*last_flag) merge_partials(g0);
+      }
     }
   }
   __syncthreads();
+  if (a.trace != nullptr && threadIdx.x == 0) {
+    trace()[kTrExit] = globaltimer_ns();
+    trace()[kTrSm] = static_cast<uint64_t>(sm_id()) | (static_cast<uint64_t>(blockIdx.x) << 32);
+    trace()[kTrUnits] = static_cast<uint64_t>(u_end - u_begin);
+  }
 }
 
 template <int NG, int NT, bool MQ, bool F16>
