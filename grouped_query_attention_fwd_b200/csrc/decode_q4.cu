@@ -59,7 +59,8 @@ constexpr int kSub = 2;                    // 16-key MMA tiles a warp takes at a
 constexpr int kChunk = 16 * kSub;          // its keys
 constexpr int kChunks = KT / kChunk;
 constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
-constexpr int kFastMerge = 4;              // split groups merged with all loads in flight
+constexpr int kFastMerge = 4;              // contributors of a split group merged directly
+constexpr int kBatch = 8;                  // partials loaded at a time by the other merge
 
 template <int NG, int NT>
 struct Q4Layout {
@@ -74,7 +75,7 @@ struct Q4Layout {
   static constexpr int kScratch = W * HP * kRow * 4;
   static constexpr int kQRows = HP * D * 2;        // Q rows of the range's second group
   static int bytes(int stages, int ragged_batch) {
-    return 128 /*alignment slack*/ + stages * kStage + kScratch + kQRows + 2 * stages * 8 + 16 +
+    return 128 /*alignment slack*/ + stages * kStage + kScratch + kQRows + (2 * stages + 2) * 8 + 32 +
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
 };
@@ -156,14 +157,18 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   uint16_t* q_next = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(scr) + L::kScratch);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(q_next) + L::kQRows);
   uint64_t* empty = full + stages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + stages);
+  uint64_t* q_full = empty + stages;     // the second group's Q rows landed
+  uint64_t* scr_free = q_full + 1;       // the scratch's states have been merged
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(scr_free + 1);
   volatile int* last_flag = abort_flag + 1;
   volatile int* fast_flag = abort_flag + 2;  // the final split group is merged here directly
   // Ticket count of the final split group, read by the producer near the end
   // of the range (kNoPeek until then).
   volatile uint32_t* peek_count = reinterpret_cast<volatile uint32_t*>(abort_flag + 3);
   constexpr uint32_t kNoPeek = 0xFFFFFFFFu;
-  int* len_s = reinterpret_cast<int*>(const_cast<int*>(abort_flag) + 4);
+  int* flushed = const_cast<int*>(abort_flag) + 4;  // warps whose state of a mid group is in the scratch
+  volatile int* mid_last = abort_flag + 5;  // the range's first group is this CTA's to merge
+  int* len_s = const_cast<int*>(abort_flag) + 8;
   int* pre_s = len_s + a.B;
 
   const int warp = threadIdx.x >> 5;
@@ -173,24 +178,36 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   auto trace = [&]() { return a.trace + blockIdx.x * kDecodeTraceWords; };  // diagnostics
   const uint64_t t_entry = (a.trace != nullptr && threadIdx.x == 0) ? globaltimer_ns() : 0;
 
-  if (threadIdx.x == W * 32) {
-    prefetch_tmap(&tmk);
-    prefetch_tmap(&tmv);
-  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], kChunks);  // one arrival per chunk
     }
+    mbar_init(q_full, 1);
+    mbar_init(scr_free, 1);
     *abort_flag = 0;
     *fast_flag = 0;
     *peek_count = kNoPeek;
+    *flushed = 0;
+    *mid_last = 0;
     fence_mbar_init();
   }
-  // From here on global memory written by earlier work on the stream is read.
-  griddep_wait();
-  griddep_launch_dependents();
+  // Q rows past the group and dims past head_dim stay zero.
+  for (int i = threadIdx.x; i < L::kQRows / 16; i += blockDim.x)
+    reinterpret_cast<uint4*>(q_next)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  Sched sc;
+  sc.pre = ragged ? pre_s : nullptr;
+  sc.len = ragged ? len_s : nullptr;
+  sc.per_b = gpb * tiles_per_group;
+  sc.gpb = gpb;
+  sc.B = a.B;
+  // Nothing global that earlier work on the stream writes is read, and nothing
+  // is written, before griddep_wait.  With lengths that is here, for every
+  // thread; without, the cut into ranges needs no memory, and each role waits
+  // right before its first access (the way there is long: cold instructions).
   if (ragged) {
+    griddep_wait();
     for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
       int len = a.lens[b];
       if (len < 0 || len > a.Sk) {
@@ -199,14 +216,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       }
       len_s[b] = len;
     }
-  }
-  __syncthreads();
-  if (a.trace != nullptr && threadIdx.x == 0) {
-    for (int w = 0; w < kDecodeTraceWords; ++w) trace()[w] = 0;
-    trace()[kTrEntry] = t_entry;
-    trace()[kTrReady] = globaltimer_ns();
-  }
-  if (ragged) {
+    __syncthreads();
     if (warp == 0) {
       // pre[b + 1] = sum over entries <= b of (groups per entry) x (tiles of the entry).
       int carry = 0;
@@ -226,19 +236,45 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       }
       if (lane == 0) pre_s[0] = 0;
     }
-    __syncthreads();
   }
-  Sched sc;
-  sc.pre = ragged ? pre_s : nullptr;
-  sc.len = ragged ? len_s : nullptr;
-  sc.per_b = gpb * tiles_per_group;
-  sc.gpb = gpb;
-  sc.B = a.B;
+  __syncthreads();
+  griddep_launch_dependents();
+  if (a.trace != nullptr && threadIdx.x == 0) {
+    for (int w = 0; w < kDecodeTraceWords; ++w) trace()[w] = 0;
+    trace()[kTrEntry] = t_entry;
+  }
   sc.total = ragged ? pre_s[a.B] : units;
   sc.P = static_cast<int>(gridDim.x) < sc.total ? static_cast<int>(gridDim.x) : sc.total;
   const bool has_range = static_cast<int>(blockIdx.x) < sc.P;
   const int u_begin = has_range ? range_start(blockIdx.x, sc.total, sc.P) : 0;
   const int u_end = has_range ? range_start(blockIdx.x + 1, sc.total, sc.P) : 0;
+
+  Cursor cu;
+  // Address of row hl (a head, or a (head, query) pair) of kv head kv of entry b.
+  auto q_row = [&](int b, int kv, int hl) {
+    const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
+    return a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
+           static_cast<int64_t>(qi) * a.qs[2];
+  };
+  // Group of a unit: its place in the launch, and who shares it.
+  struct Group {
+    int b, kv, pass, id, beg, tiles, c_lo, c_hi, rows;
+  };
+  auto group_at = [&](int u) {
+    seek(cu, u, sc, a);
+    const int gi = (u - cu.beg) / cu.kr.tiles;
+    Group g;
+    g.b = cu.b;
+    g.kv = gi / passes;
+    g.pass = gi % passes;
+    g.id = cu.b * gpb + gi;
+    g.beg = cu.beg + gi * cu.kr.tiles;
+    g.tiles = cu.kr.tiles;
+    g.c_lo = cta_of_unit(g.beg, sc.total, sc.P);
+    g.c_hi = cta_of_unit(g.beg + g.tiles - 1, sc.total, sc.P);
+    g.rows = min(HP, a.rows - g.pass * HP);
+    return g;
+  };
 
   if (warp == W) {
     // ------------------------------------------------------------ producer
@@ -252,15 +288,27 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     const bool paged = a.bt != nullptr;
     int it = 0, s = 0;          // units issued; stage of the next one
     uint32_t parity = 1;        // of the wait for a free stage (passes at once in round 0)
-    bool ok = true;
-    Cursor cu;
+    bool ok = true, q_sent = false;
+    if (lane == 0) {
+      prefetch_tmap(&tmk);
+      prefetch_tmap(&tmv);
+    }
     for (int ua = u_begin; ua < u_end && ok;) {
-      seek(cu, ua, sc, a);
-      const int gi = (ua - cu.beg) / cu.kr.tiles;
-      const int g_beg = cu.beg + gi * cu.kr.tiles;
-      const int ub = min(u_end, g_beg + cu.kr.tiles);
-      const int kv = gi / passes, b = cu.b;
-      int key0 = (ua - g_beg + cu.kr.t0) * KT;
+      const Group grp = group_at(ua);
+      const int ub = min(u_end, grp.beg + grp.tiles);
+      const int kv = grp.kv, b = grp.b;
+      int key0 = (ua - grp.beg + cu.kr.t0) * KT;
+      if (ua == u_begin && !ragged) {
+        // Contiguous caches: the first units start towards L2 before the grid
+        // dependency resolves (earlier work may still be writing the cache;
+        // these are hints, the copies below read what it wrote).
+        if (!paged && lane < 2 && ua + lane < ub) {
+          tma_prefetch_4d(&tmk, 0, key0 + lane * KT, kv, b);
+          tma_prefetch_4d(&tmv, 0, key0 + lane * KT, kv, b);
+        }
+        griddep_wait();
+      }
+      if (a.trace != nullptr && lane == 0 && ua == u_begin) trace()[kTrReady] = globaltimer_ns();
       const int len = sc.len ? sc.len[b] : a.Sk;
       // Page and row of a 64-key box; one past the sequence's length takes
       // page num_pages, which is out of range: TMA fills it with zeros.
@@ -325,6 +373,20 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           }
         }
       }
+      if (ua == u_begin && ub < u_end && ok) {
+        // The Q rows of the range's second group: at the change of groups
+        // they would cost the consumers a round trip.  (The first group's
+        // come while its first unit does; a range over more groups has short
+        // ones, and the consumers fetch the others' when they get there.)
+        const Group next = group_at(ub);
+        if (lane == 0)
+          mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(next.rows * a.Dv * 2));
+        __syncwarp();
+        if (lane < next.rows)
+          bulk_load(q_next + lane * D, q_row(next.b, next.kv, next.pass * HP + lane),
+                    static_cast<uint32_t>(a.Dv * 2), q_full);
+        q_sent = true;
+      }
       ua = ub;
     }
     if (lane == 0) {
@@ -352,38 +414,12 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         for (int j = it > stages ? it - stages : 0; j < it; ++j)
           mbar_wait_drain(&full[j % stages], static_cast<uint32_t>((j / stages) & 1),
                           a.wait_ns / 4);
+      if (*abort_flag && q_sent) mbar_wait_drain(q_full, 0, a.wait_ns / 4);
     }
   } else {
     // ------------------------------------------------------------ consumers
     const int c = lane & 3, r8 = lane >> 2;
     auto sync_consumers = [] { asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory"); };
-    Cursor cu;
-    // Address of row hl (a head, or a (head, query) pair) of kv head kv of entry b.
-    auto q_row = [&](int b, int kv, int hl) {
-      const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
-      return a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
-             static_cast<int64_t>(qi) * a.qs[2];
-    };
-    int mid_ticket = -1;  // thread 0: the first group's ticket, taken before the range's end
-    // Group of a unit: its place in the launch, and who shares it.
-    struct Group {
-      int b, kv, pass, id, beg, tiles, c_lo, c_hi, rows;
-    };
-    auto group_at = [&](int u) {
-      seek(cu, u, sc, a);
-      const int gi = (u - cu.beg) / cu.kr.tiles;
-      Group g;
-      g.b = cu.b;
-      g.kv = gi / passes;
-      g.pass = gi % passes;
-      g.id = cu.b * gpb + gi;
-      g.beg = cu.beg + gi * cu.kr.tiles;
-      g.tiles = cu.kr.tiles;
-      g.c_lo = cta_of_unit(g.beg, sc.total, sc.P);
-      g.c_hi = cta_of_unit(g.beg + g.tiles - 1, sc.total, sc.P);
-      g.rows = min(HP, a.rows - g.pass * HP);
-      return g;
-    };
     // Output row hr of a group's pass, dims 4 d4 .. + 3.
     auto write_out = [&](const Group& g, int hr, int d4, float lsum, const float4& acc) {
       if (4 * d4 >= a.Dv) return;
@@ -403,75 +439,58 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       const int first = group_of(range_start(cta, sc.total, sc.P), sc, a);
       return (cta * 2 + (first == id ? 0 : 1)) * HP;
     };
-    // All partials of a split group are published: their merge, by the whole
-    // consumer group, through the scratch.
+    // All partials of a split group are published: their merge by the whole
+    // consumer group, eight contributors' loads in flight at a time.
     auto merge_partials = [&](const Group& g) {
       const int n = g.c_hi - g.c_lo + 1;
-      int* slot = reinterpret_cast<int*>(scr);  // n slots
-      float* wt = scr + ((n + 31) / 32) * 32;   // n x HP weights
-      float* lsum = wt + n * HP;                // HP sums
+      int* slot = reinterpret_cast<int*>(scr);
       for (int k = threadIdx.x; k < n; k += W * 32) slot[k] = slot_of(g.c_lo + k, g.id);
-      sync_consumers();
-      for (int hr = warp; hr < g.rows; hr += W) {  // one warp per row
-        float M = -INFINITY;
-        for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(&a.part_ml[slot[k] + hr]).x);
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
-        const float ref = exp_ref(M);
-        float ls = 0.f;
-        for (int k = lane; k < n; k += 32) {
-          const float2 ml = __ldcg(&a.part_ml[slot[k] + hr]);
-          const float w = fast_exp2(ml.x - ref);
-          wt[k * HP + hr] = w;
-          ls = fmaf(w, ml.y, ls);
-        }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, i);
-        if (lane == 0) lsum[hr] = ls;
-      }
       sync_consumers();
       for (int i = threadIdx.x; i < g.rows * (D / 4); i += W * 32) {
         const int hr = i / (D / 4), d4 = i % (D / 4);
+        float M = -INFINITY, lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-          const float w = wt[k * HP + hr];
-          const float4 ov = __ldcg(reinterpret_cast<const float4*>(
-              &a.part_o[static_cast<int64_t>(slot[k] + hr) * D + 4 * d4]));
-          acc.x = fmaf(w, ov.x, acc.x);
-          acc.y = fmaf(w, ov.y, acc.y);
-          acc.z = fmaf(w, ov.z, acc.z);
-          acc.w = fmaf(w, ov.w, acc.w);
+        for (int k0 = 0; k0 < n; k0 += kBatch) {
+          float2 ml[kBatch];
+          float4 ov[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            ov[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < n) {
+              const int64_t at = slot[k0 + k] + hr;
+              ml[k] = __ldcg(&a.part_ml[at]);
+              ov[k] = __ldcg(reinterpret_cast<const float4*>(&a.part_o[at * D + 4 * d4]));
+            }
+          }
+          float top = M;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+          const float ref = exp_ref(top), old = fast_exp2(M - ref);
+          M = top;
+          lsum *= old;
+          acc.x *= old;
+          acc.y *= old;
+          acc.z *= old;
+          acc.w *= old;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            const float w = fast_exp2(ml[k].x - ref);
+            lsum = fmaf(w, ml[k].y, lsum);
+            acc.x = fmaf(w, ov[k].x, acc.x);
+            acc.y = fmaf(w, ov[k].y, acc.y);
+            acc.z = fmaf(w, ov[k].z, acc.z);
+            acc.w = fmaf(w, ov[k].w, acc.w);
+          }
         }
-        write_out(g, hr, d4, lsum[hr], acc);
+        write_out(g, hr, d4, lsum, acc);
       }
       if (threadIdx.x == 0) atomicExch(&counters[g.id], 0u);
       sync_consumers();
     };
 
-    // The Q rows of the range's second group are fetched now: at the change
-    // of groups they would cost a round trip.  (The first group's come while
-    // its first unit does; a range over more groups has short ones, and
-    // fetches the others' when it gets there.)
-    int u_second = u_end;
-    if (u_begin < u_end) {
-      const Group g0 = group_at(u_begin);
-      u_second = g0.beg + g0.tiles;
-      if (u_second < u_end) {
-        const Group g1 = group_at(u_second);
-        for (int i = threadIdx.x; i < HP * (D / 8); i += W * 32) {
-          const int hr = i / (D / 8), d8 = i % (D / 8);
-          uint16_t* dst = q_next + i * 8;
-          if (hr < g1.rows && d8 * 8 < a.Dv)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                         "l"(q_row(g1.b, g1.kv, g1.pass * HP + hr) + d8 * 8)
-                         : "memory");
-          else
-            *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-    }
-
+    int n_flush = 0;           // groups whose states went through the scratch
+    int u_second = u_end;      // first unit of the range's second group
     for (int ua = u_begin; ua < u_end;) {
       // One group (kv head and pass of one entry): units [ua, ub) of this range.
       const Group grp = group_at(ua);
@@ -479,6 +498,14 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       const int tile0 = ua - grp.beg + cu.kr.t0;
       const int kv = grp.kv, pass = grp.pass, b = grp.b;
       const int len = sc.len ? sc.len[b] : a.Sk;
+      if (ua == u_begin) {
+        u_second = ub;
+        if (!ragged) griddep_wait();
+      }
+      // (A wait that gave up sets the abort flag: the arithmetic goes on with
+      // whatever is there, the result is undefined.)
+      const bool stashed = ua == u_second;
+      if (stashed) mbar_wait(q_full, 0, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
 
       // Q as B fragments, thread (r8, c): row r8 of each column tile, dims
       // 32 t + 8 c .. + 7; and the sums over each group's dims, the factors
@@ -491,7 +518,6 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int hl = pass * HP + nt * 8 + r8;
-        const bool stashed = ua == u_second;
         const uint16_t* qrow = stashed ? q_next + (nt * 8 + r8) * D : q_row(b, kv, hl);
         float f[NG][8];
         float amax = 0.f;
@@ -799,8 +825,11 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         }
         *fast_flag = fast;
       }
-      if (ua != u_begin) sync_consumers();  // the last group's states have been read
-      asm volatile("cp.async.wait_all;" ::: "memory");  // (visible to all after the barrier)
+      // The scratch is free once the last group's states have been merged.
+      if (n_flush > 0)
+        mbar_wait(scr_free, static_cast<uint32_t>((n_flush - 1) & 1), abort_flag, a.err,
+                  kErrDecodeWait, a.wait_ns);
+      ++n_flush;
       float* mine = scr + warp * HP * R;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -824,11 +853,6 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           }
           if (r8 == 0) *reinterpret_cast<float2*>(mine + h * R + D) = make_float2(m_ref[nt][e], lv);
         }
-      sync_consumers();
-      if (a.trace != nullptr && threadIdx.x == 0) {
-        trace()[kTrFlushes] += 1;
-        if (final_group) trace()[kTrFinalMerged] = globaltimer_ns();
-      }
       const int quads = grp.rows * (D / 4);
       // Row hr of the pass, dims 4 d4 .. + 3 over the W states: (M, l, O).
       auto merge_warps = [&](int hr, int d4, float& M, float& lsum, float4& acc) {
@@ -850,14 +874,61 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           acc.w = fmaf(wt, ov.w, acc.w);
         }
       };
-      if (n_contrib == 1) {
-        for (int i = threadIdx.x; i < quads; i += W * 32) {
+      // Quads i0, i0 + step, ...: written out (a whole group), or published as
+      // this CTA's partial (a split one).
+      auto merge_and_store = [&](int i0, int step) {
+        const int base = n_contrib > 1 ? slot_of(blockIdx.x, grp.id) : 0;
+        for (int i = i0; i < quads; i += step) {
+          const int hr = i / (D / 4), d4 = i % (D / 4);
           float M, lsum;
           float4 acc;
-          merge_warps(i / (D / 4), i % (D / 4), M, lsum, acc);
-          write_out(grp, i / (D / 4), i % (D / 4), lsum, acc);
+          merge_warps(hr, d4, M, lsum, acc);
+          if (n_contrib == 1) {
+            write_out(grp, hr, d4, lsum, acc);
+          } else {
+            const int64_t at = base + hr;
+            *reinterpret_cast<float4*>(&a.part_o[at * D + 4 * d4]) = acc;
+            if (d4 == 0) a.part_ml[at] = make_float2(M, lsum);
+          }
         }
-      } else if (final_group && *fast_flag) {
+      };
+      if (!final_group) {
+        // The range goes on: the warp that comes last merges the states by
+        // itself, the others are already at the next group.
+        __syncwarp();
+        int last = 0;
+        if (lane == 0) {
+          fence_acq_rel_cta();
+          last = atomicAdd(flushed, 1) == W - 1;
+          if (last) {
+            *flushed = 0;
+            fence_acq_rel_cta();
+          }
+        }
+        last = __shfl_sync(0xffffffffu, last, 0);
+        if (last) {
+          merge_and_store(lane, 32);
+          __syncwarp();
+          if (lane == 0) {
+            // (The add at gpu scope publishes the warp's stores.)
+            if (n_contrib > 1 &&
+                atom_add_acq_rel_gpu(&counters[grp.id], 1u) == static_cast<uint32_t>(n_contrib - 1))
+              *mid_last = 1;
+            mbar_arrive(scr_free);
+            if (a.trace != nullptr) trace()[kTrFlushes] += 1;
+          }
+        }
+        ua = ub;
+        continue;
+      }
+      sync_consumers();
+      if (a.trace != nullptr && threadIdx.x == 0) {
+        trace()[kTrFlushes] += 1;
+        trace()[kTrFinalMerged] = globaltimer_ns();
+      }
+      if (n_contrib == 1) {
+        merge_and_store(threadIdx.x, W * 32);
+      } else if (*fast_flag) {
         // Every other partial is published: merge them with these states.
         for (int i = threadIdx.x; i < quads; i += W * 32) {
           const int hr = i / (D / 4), d4 = i % (D / 4);
@@ -900,37 +971,17 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         // All have arrived: the counter goes back to zero for the next launch.
         if (threadIdx.x == 0) counters[grp.id] = 0u;
       } else {
-        // Publish a partial and take a ticket.
-        const int base = slot_of(blockIdx.x, grp.id);
-        for (int i = threadIdx.x; i < quads; i += W * 32) {
-          const int hr = i / (D / 4), d4 = i % (D / 4);
-          float M, lsum;
-          float4 acc;
-          merge_warps(hr, d4, M, lsum, acc);
-          *reinterpret_cast<float4*>(&a.part_o[static_cast<int64_t>(base + hr) * D + 4 * d4]) = acc;
-          if (d4 == 0) a.part_ml[base + hr] = make_float2(M, lsum);
-        }
-        if (!final_group) {
-          // The range goes on: only warp 0 waits for the others' stores, and
-          // whether this was the group's last ticket is looked at at the end.
-          if (warp == 0) {
-            asm volatile("bar.sync 2, %0;" ::"n"(W * 32) : "memory");
-            if (lane == 0)
-              mid_ticket = static_cast<int>(atom_add_acq_rel_gpu(&counters[grp.id], 1u));
-          } else {
-            asm volatile("bar.arrive 2, %0;" ::"n"(W * 32) : "memory");
-          }
-        } else {
-          // (The barrier makes every thread's partial visible to thread 0; its
-          // acquire-release add publishes them and, for the last arriver,
-          // makes the others' visible.)
-          sync_consumers();
-          if (threadIdx.x == 0)
-            *last_flag = atom_add_acq_rel_gpu(&counters[grp.id], 1u) ==
-                         static_cast<uint32_t>(n_contrib - 1);
-          sync_consumers();
-          if (*last_flag) merge_partials(grp);
-        }
+        // Publish a partial and take a ticket; the last to do so merges.  (The
+        // barrier makes every thread's partial visible to thread 0; its
+        // acquire-release add publishes them and, for the last arriver, makes
+        // the others' visible.)
+        merge_and_store(threadIdx.x, W * 32);
+        sync_consumers();
+        if (threadIdx.x == 0)
+          *last_flag = atom_add_acq_rel_gpu(&counters[grp.id], 1u) ==
+                       static_cast<uint32_t>(n_contrib - 1);
+        sync_consumers();
+        if (*last_flag) merge_partials(grp);
       }
       if (a.trace != nullptr && threadIdx.x == 0 && final_group) {
         trace()[kTrFinalDone] = globaltimer_ns();
@@ -938,16 +989,12 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       }
       ua = ub;
     }
-    // The first group, where it ended before the range did and this CTA was
-    // the last of its contributors.
+    // The range's first group, where it ended before the range did and this
+    // CTA turned out to be the last of its contributors.  (Its merge, before
+    // the final group's, set the flag.)
     if (u_second < u_end) {
-      const Group g0 = group_at(u_begin);
-      if (g0.c_lo != g0.c_hi) {
-        sync_consumers();
-        if (threadIdx.x == 0) *last_flag = mid_ticket == g0.c_hi - g0.c_lo;
-        sync_consumers();
-        if (*last_flag) merge_partials(g0);
-      }
+      sync_consumers();
+      if (*mid_last) merge_partials(group_at(u_begin));
     }
   }
   __syncthreads();
