@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -116,6 +117,16 @@ int device_sm_count(int* out) {
     cudaGetLastError();
     return GQA_ERR_DEVICE;
   }
+  // A device's properties never change: asked once per device.
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  if (dev >= 0 && dev < kMaxDevices) {
+    const int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms > 0) {
+      *out = sms;
+      return GQA_OK;
+    }
+  }
   int sms = 0, major = 0;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) {
@@ -123,6 +134,7 @@ int device_sm_count(int* out) {
     return GQA_ERR_DEVICE;
   }
   if (major != 10) return GQA_ERR_DEVICE;
+  if (dev >= 0 && dev < kMaxDevices) known[dev].store(sms, std::memory_order_relaxed);
   *out = sms;
   return GQA_OK;
 }

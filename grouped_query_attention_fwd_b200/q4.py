@@ -10,12 +10,13 @@ problem descriptor of the first such call; pointers are taken anew each time.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import threading
 
 from . import (GQA_DTYPE_BF16, GQA_DTYPE_F16, GQA_OK, GQAError, Plan, Problem, _lens_ptr, _lib,
-               _offset, _stream_object, _table, _torch, make_problem, workspace_for)
+               _offset, _stream_object, _table, _torch, _workspaces, make_problem, workspace_for)
 
 _vp = ctypes.c_void_p
 
@@ -53,14 +54,12 @@ _seen = threading.local()
 _MAX_SEEN = 1024
 
 
-def _remember(kind, key, make):
-    seen = _seen.__dict__.setdefault(kind, {})
-    got = seen.get(key)
-    if got is None:
-        if len(seen) >= _MAX_SEEN:
-            seen.clear()
-        got = seen[key] = make()
-    return got
+def _remember(kind, key, value):
+    seen = getattr(_seen, kind)
+    if len(seen) >= _MAX_SEEN:
+        seen.clear()
+    seen[key] = value
+    return value
 
 
 def q4_record_bytes(head_dim: int) -> int:
@@ -80,68 +79,68 @@ def _half(dtype) -> int:
     raise TypeError("a 4-bit cache serves bfloat16 and float16, got %s" % dtype)
 
 
-def _check_caches(cache_k, cache_v, device):
+def _check_caches(cache_k, cache_v):
     torch = _torch()
-    for c in (cache_k, cache_v):
-        if c.dtype is not torch.uint8 or c.dim() != 4:
-            raise TypeError("a 4-bit cache is a uint8 tensor [B, Hkv, capacity, record], or a "
-                            "pool [num_pages, Hkv, page_size, record]")
-        if c.device != device:
-            raise ValueError("all tensors must be on the same CUDA device")
+    if cache_k.dtype is not torch.uint8 or cache_v.dtype is not torch.uint8 or cache_k.dim() != 4:
+        raise TypeError("a 4-bit cache is a uint8 tensor [B, Hkv, capacity, record], or a pool "
+                        "[num_pages, Hkv, page_size, record]")
     if cache_k.shape != cache_v.shape:
         raise ValueError("the K and V caches must have one shape")
 
 
-def _same_device(device, *tensors):
-    if device.type != "cuda":
+def _device_of(first, *others) -> int:
+    """Index of the CUDA device that all tensors (or None) are on."""
+    idx = first.get_device()
+    if idx < 0:
         raise ValueError("the 4-bit cache takes CUDA tensors only (there is no CPU path)")
-    for t in tensors:
-        if t is not None and t.device != device:
+    for t in others:
+        if t is not None and t.get_device() != idx:
             raise ValueError("all tensors must be on the same CUDA device")
+    return idx
 
 
-class _On:
-    """Makes a device and the stream of a call current (nothing to do where they are)."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        self.idx = device.index
-        self.contexts = []
-        if torch.cuda.current_device() != self.idx:
-            self.contexts.append(torch.cuda.device(self.idx))
-        cur = torch.cuda.current_stream(self.idx)
-        self.stream = cur.cuda_stream
-        if stream is not None and int(stream) != self.stream:
-            self.contexts.append(torch.cuda.stream(_stream_object(self.idx, stream)))
-            self.stream = int(stream)
-
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
-        return False
+def _contexts(idx, stream):
+    """What a call has to enter so that its device and its stream are current:
+    nothing, mostly."""
+    torch = _torch()
+    got = []
+    if torch._C._cuda_getDevice() != idx:
+        got.append(torch.cuda.device(idx))
+    if stream is not None and int(stream) != torch._C._cuda_getCurrentRawStream(idx):
+        got.append(torch.cuda.stream(_stream_object(idx, stream)))
+    return got
 
 
 _HEAD = 256 + 65536  # error word, append ticket and decode tickets: what has to start at zero
 
 
-def _workspace(on, nbytes, workspace):
-    """The caller's workspace, the cached one of the stream, or, in a capture,
-    one that belongs to the graph alone (zeroed by each replay): graphs
-    replayed side by side never share one."""
+def _workspace(idx, nbytes, workspace):
+    """The caller's workspace, the cached one of the current stream, or, in a
+    capture, one that belongs to the graph alone (zeroed by each replay):
+    graphs replayed side by side never share one."""
     if workspace is not None:
         return workspace
     torch = _torch()
-    if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8,
-                         device=torch.device("cuda", on.idx))
+    if torch._C._cuda_isCurrentStreamCapturing():
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
         ws[:_HEAD].zero_()
         return ws
-    return workspace_for(torch.device("cuda", on.idx), nbytes, on.stream)
+    stream = torch._C._cuda_getCurrentRawStream(idx)
+    ws = _workspaces.get((idx, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = workspace_for(torch.device("cuda", idx), nbytes, stream)
+    return ws
+
+
+def _enter(idx, stream, call, *args):
+    """call(stream handle, *args) with the device and the stream current."""
+    contexts = _contexts(idx, stream)
+    if not contexts:
+        return call(_torch()._C._cuda_getCurrentRawStream(idx), *args)
+    with contextlib.ExitStack() as stack:
+        for c in contexts:
+            stack.enter_context(c)
+        return call(_torch()._C._cuda_getCurrentRawStream(idx), *args)
 
 
 # ------------------------------------------------------------ append and read back
@@ -188,25 +187,29 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
     False leaves it, for layers that share one tensor of lengths.  An entry
     that does not fit is left as it was and device_status() reports
     GQA_ERR_KV_LENGTH."""
-    device = k_new.device
-    _same_device(device, v_new, kv_lens, new_lens, block_table)
-    _check_caches(cache_k, cache_v, device)
+    idx = _device_of(k_new, v_new, kv_lens, cache_k, cache_v, new_lens, block_table)
+    _check_caches(cache_k, cache_v)
     if k_new.dim() != 4 or v_new.dtype is not k_new.dtype:
         raise TypeError("k_new and v_new must be [B, Hkv, n, D] of one type")
     B = k_new.shape[0]
     bt = _table(block_table, B)[0] if block_table is not None else None
     key = (k_new.dtype, k_new.shape, k_new.stride(), v_new.shape, v_new.stride(), cache_k.shape,
-           cache_k.stride(), cache_v.stride(), bool(advance),
+           cache_k.stride(), cache_v.stride(), advance,
            None if bt is None else (block_table.shape, block_table.stride(0)))
-    d = _remember("append", key, lambda: _rows_desc(
-        k_new.dtype, cache_k, cache_v, k_new, v_new, k_new.shape[3], block_table, advance))
+    d = _seen.__dict__.setdefault("append", {}).get(key)
+    if d is None:
+        d = _remember("append", key, _rows_desc(k_new.dtype, cache_k, cache_v, k_new, v_new,
+                                                k_new.shape[3], block_table, bool(advance)))
     d.block_table = bt
     d.counts = None if new_lens is None else _int32(new_lens, B, "new_lens")
     lens = _int32(kv_lens, B, "kv_lens")
-    with _On(device, stream) as on:
-        ws = _workspace(on, 256, workspace)
-        rc = _lib.gqa_kv_append_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k_new.data_ptr(),
-                                   v_new.data_ptr(), lens, ws.data_ptr(), ws.numel(), on.stream)
+
+    def call(handle):
+        ws = _workspace(idx, 256, workspace)
+        return _lib.gqa_kv_append_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k_new.data_ptr(),
+                                     v_new.data_ptr(), lens, ws.data_ptr(), ws.numel(), handle)
+
+    rc = _enter(idx, stream, call)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_kv_append_q4")
 
@@ -219,13 +222,11 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
     int, or an int32 CUDA tensor [B].  n defaults to the rest of the capacity.
     Rows at or past kv_lens[b] (the capacity without it) are zeros."""
     torch = _torch()
-    device = cache_k.device
     starts = start if isinstance(start, torch.Tensor) else None
-    _same_device(device, kv_lens, starts, out_k, out_v, block_table)
-    _check_caches(cache_k, cache_v, device)
-    B = cache_k.shape[0]
+    idx = _device_of(cache_k, cache_v, kv_lens, starts, out_k, out_v, block_table)
+    _check_caches(cache_k, cache_v)
+    B, Hkv, capacity, _ = cache_k.shape
     bt = None
-    capacity = cache_k.shape[2]
     if block_table is not None:
         B = block_table.shape[0]
         bt = _table(block_table, B)[0]
@@ -234,27 +235,30 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
         n = capacity - (0 if starts is not None else int(start))
     if n < 0:
         raise ValueError("n must not be negative")
-    shape = (B, cache_k.shape[1], int(n), int(head_dim))
-    with _On(device, stream) as on:
-        outs = []
-        for t in (out_k, out_v):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=device)
-            elif tuple(t.shape) != shape or t.dtype is not dtype:
-                raise ValueError("out_k and out_v must be [B, Hkv, n, D] of the given type")
-            outs.append(t)
-        k, v = outs
+    shape = (B, Hkv, int(n), int(head_dim))
+    for t in (out_k, out_v):
+        if t is not None and (t.shape != shape or t.dtype is not dtype):
+            raise ValueError("out_k and out_v must be [B, Hkv, n, D] of the given type")
+
+    def call(handle):
+        k = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_k is None else out_k
+        v = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_v is None else out_v
         key = (dtype, shape, k.stride(), v.stride(), cache_k.shape, cache_k.stride(),
                cache_v.stride(), None if bt is None else (block_table.shape, block_table.stride(0)))
-        d = _remember("read", key, lambda: _rows_desc(
-            dtype, cache_k, cache_v, k, v, shape[3], block_table, False))
+        d = _seen.__dict__.setdefault("read", {}).get(key)
+        if d is None:
+            d = _remember("read", key, _rows_desc(dtype, cache_k, cache_v, k, v, shape[3],
+                                                  block_table, False))
         d.block_table = bt
         d.starts = None if starts is None else _int32(starts, B, "start")
         d.start = 0 if starts is not None else int(start)
         lens = None if kv_lens is None else _int32(kv_lens, B, "kv_lens")
-        ws = _workspace(on, 256, workspace)
+        ws = _workspace(idx, 256, workspace)
         rc = _lib.gqa_kv_read_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k.data_ptr(),
-                                 v.data_ptr(), lens, ws.data_ptr(), ws.numel(), on.stream)
+                                 v.data_ptr(), lens, ws.data_ptr(), ws.numel(), handle)
+        return rc, k, v
+
+    rc, k, v = _enter(idx, stream, call)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_kv_read_q4")
     return k, v
@@ -323,36 +327,36 @@ def forward_q4(q, cache_k, cache_v, mask=None, causal=False, scale=None, out=Non
     q and the result are bf16 or fp16, the type the cache was written with;
     every other argument is ``forward``'s."""
     torch = _torch()
-    device = q.device
-    _same_device(device, mask, kv_lens, block_table, out)
-    _check_caches(cache_k, cache_v, device)
+    idx = _device_of(q, cache_k, cache_v, mask, kv_lens, block_table, out)
+    _check_caches(cache_k, cache_v)
     if mask is not None:
         if mask.dtype is torch.bool:
             mask = mask.view(torch.uint8)
         elif mask.dtype is not torch.uint8:
             raise TypeError("mask must be bool or uint8")
-    with _On(device, stream) as on:
-        if out is None:
-            # q's shape, laid out afresh: [B, Hq, Sq, D] contiguous
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        key = (q.dtype, q.shape, q.stride(), out.shape, out.dtype, out.stride(), cache_k.shape,
+
+    def call(handle, o):
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        key = (q.dtype, q.shape, q.stride(), o.shape, o.dtype, o.stride(), cache_k.shape,
                cache_k.stride(), cache_v.stride(),
-               None if mask is None else (mask.shape, mask.stride()), bool(causal), scale,
-               causal_offset, window, kv_lens is None, on.idx,
+               None if mask is None else (mask.shape, mask.stride()), causal, scale,
+               causal_offset, window, kv_lens is None, idx,
                None if block_table is None else (block_table.shape, block_table.stride(0)))
-
-        def make():
-            p = q4_problem_for(q, cache_k, cache_v, mask, causal, scale, out, causal_offset,
+        known = _seen.__dict__.setdefault("forward", {}).get(key)
+        if known is None:
+            p = q4_problem_for(q, cache_k, cache_v, mask, causal, scale, o, causal_offset,
                                window, kv_lens, block_table)
-            return p, _query(p).workspace_bytes
-
-        p, nbytes = _remember("forward", key, make)
+            known = _remember("forward", key, (p, _query(p).workspace_bytes))
+        p, nbytes = known
         p.kv_lens = None if kv_lens is None else _int32(kv_lens, q.shape[0], "kv_lens")
         p.block_table = None if block_table is None else _table(block_table, q.shape[0])[0]
-        ws = _workspace(on, nbytes, workspace)
-        rc = _lib.gqa_forward_q4(p, q.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(),
-                                 mask.data_ptr() if mask is not None else None, out.data_ptr(),
-                                 ws.data_ptr(), ws.numel(), on.stream)
+        ws = _workspace(idx, nbytes, workspace)
+        return _lib.gqa_forward_q4(p, q.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(),
+                                   mask.data_ptr() if mask is not None else None, o.data_ptr(),
+                                   ws.data_ptr(), ws.numel(), handle), o
+
+    rc, out = _enter(idx, stream, call, out)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_forward_q4")
     return out
