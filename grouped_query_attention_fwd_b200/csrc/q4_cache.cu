@@ -1,15 +1,27 @@
 // Writing rows into a 4-bit cache and reading them back.
 //
-// Four lanes share a group of 32 values, eight values (16 bytes of the 16-bit
-// row, one 32-bit word of codes) each, so a warp covers eight groups and both
-// sides of the copy are contiguous.  The group's minimum and maximum are a
-// two-step butterfly over the four lanes.  Both kernels move each byte once
-// and are bound by HBM (a few launches' worth of rows) or by the launch.
+// Append: one thread takes one group of 32 values (four 16-byte loads in
+// flight, 16 bytes of codes and 4 of parameters out), or, where that would
+// leave most of the machine idle, four threads share one (eight values each, a
+// two-step butterfly for minimum and maximum): 4 x 4096 tokens of 8 heads take
+// 29 us one way and 61 us the other, 16 single tokens the other way round
+// 0.6 us less.  Consecutive threads take the groups of a row, then rows, so
+// that a warp's loads and stores cover whole sectors.
 //
-// The code of a value is the correctly rounded fp32 quotient (x - min) /
-// scale, rounded to nearest even: the borders between codes, (k + 1/2) *
-// scale, are exact in fp32, so a correctly rounded quotient never falls on
-// the wrong side of one.
+// The code of a value is rint((x - min) / scale).  A division per value would
+// cost more than the rest: the quotient is taken as a product with the
+// reciprocal, at most one code off, and the remainder (x - min) - code *
+// scale, exact in one fused multiply-add, says where: only when it reaches
+// half a scale.  (The borders (k + 1/2) * scale are exact in fp32, so that the
+// rounded quotient, too, is on a border only if the remainder is half a scale:
+// ties go to the even code either way.)
+//
+// Read back: a thread takes eight dims (a 32-bit word of codes, 16 bytes out)
+// of kRows rows, their loads all in flight before the first is used; nothing
+// but the row changes between them (no division per piece).
+//
+// Both move each byte once: bound by HBM for long prompts, by the launch for
+// single tokens.
 #include <cuda_runtime.h>
 
 #include "kernels.h"
@@ -22,6 +34,7 @@ namespace {
 using namespace q4;
 
 constexpr int kThreads = 256;
+constexpr double kManyPieces = 148.0 * 2048 * 4;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -32,29 +45,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
-}
-
-// What one lane works on: eight values of a group of one row.
-struct Piece {
-  int kv, b, h, t, g, d0;  // tensor (0 K, 1 V), entry, head, row, group, first value
-};
-
-// Piece x of the 2 * B * H * n rows, 4 * G lanes each; rows fastest in t.
-__device__ __forceinline__ Piece piece_of(uint32_t x, const Q4RowsArgs& a, int G) {
-  Piece p;
-  const uint32_t lanes = 4u * static_cast<uint32_t>(G);
-  uint32_t row = x / lanes;
-  const uint32_t r = x - row * lanes;
-  p.g = static_cast<int>(r >> 2);
-  p.d0 = static_cast<int>(r) * 8;
-  uint32_t y = row / static_cast<uint32_t>(a.n);
-  p.t = static_cast<int>(row - y * static_cast<uint32_t>(a.n));
-  row = y;
-  y = row / static_cast<uint32_t>(a.H);
-  p.h = static_cast<int>(row - y * static_cast<uint32_t>(a.H));
-  p.kv = y >= static_cast<uint32_t>(a.B) ? 1 : 0;
-  p.b = static_cast<int>(y) - p.kv * a.B;
-  return p;
 }
 
 // Byte offset of row j of entry b, head h in a cache, or -1: a page outside the pool.
@@ -73,75 +63,174 @@ __device__ __forceinline__ int count_of(const Q4RowsArgs& a, int b, int64_t len)
   return c;
 }
 
+// Larger / smaller of two packed 16-bit pairs; a NaN stays.
 template <bool F16>
-__global__ void __launch_bounds__(kThreads) gqa_q4_append_kernel(const Q4RowsArgs a,
-                                                                 const uint32_t pieces) {
-  griddep_launch_dependents();  // as in the 16-bit append
-  const int G = groups_of(a.D);
-  // Every lane of a group's four takes the same branches (pieces is a
-  // multiple of 4, and so is the stride).
-  for (uint32_t x = blockIdx.x * kThreads + threadIdx.x; x < pieces; x += gridDim.x * kThreads) {
-    const Piece p = piece_of(x, a, G);
-    const uint32_t quad = 0xFu << (lane_id() & 28u);
-    const int64_t len = a.lens[p.b];
-    const int count = count_of(a, p.b, len);
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if (F16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if (F16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
+// Codes of eight values (four packed words), as the nibbles of one word.
+template <bool F16>
+__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4], float lo, float s, float r,
+                                             float half) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  uint32_t word = 0;
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = __fsub_rn(to_f32<F16>((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu), lo);
+    const float c = __fmaf_rn(d, r, kMagic);
+    const float rest = __fmaf_rn(-__fsub_rn(c, kMagic), s, d);
+    near = near || fabsf(rest) >= half;
+    word += __float_as_uint(c) << (4 * i);
+  }
+  word -= 0x4B400000u * 0x11111111u;  // the magic number's bits of all eight
+  if (near) {
+    word = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = __fsub_rn(to_f32<F16>((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu), lo);
+      const float c = __fmaf_rn(d, r, kMagic);
+      const float rest = __fmaf_rn(-__fsub_rn(c, kMagic), s, d);
+      uint32_t n = __float_as_uint(c) - 0x4B400000u;
+      const bool odd = (n & 1u) != 0u;
+      if (rest > half || (rest == half && odd)) ++n;
+      if (rest < -half || (rest == -half && odd)) --n;
+      word |= n << (4 * i);
+    }
+  }
+  return word;
+}
+
+// The same by division, clamped: for subnormal scales, whose reciprocal may be
+// infinite and which may be far below a fifteenth of the spread.
+template <bool F16>
+__device__ __forceinline__ uint32_t codes_by_division(const uint32_t (&w)[4], float lo, float s) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = to_f32<F16>((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu);
+    word |= static_cast<uint32_t>(fminf(rintf(__fdiv_rn(__fsub_rn(x, lo), s)), 15.f)) << (4 * i);
+  }
+  return word;
+}
+
+// LPG: threads that share a group (1 or 4).
+template <bool F16, int G, int LPG>
+__global__ void __launch_bounds__(kThreads) gqa_q4_append_kernel(const Q4RowsArgs a) {
+  // A decode launched after this one as a programmatic dependent may start its
+  // prologue now; this kernel itself may have started before its predecessor
+  // ended, and touches memory only after it has.
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int L = G * LPG, K = 4 / LPG;         // threads of a row; eight-value words of a thread
+  const int rows_per_block = blockDim.x / L;      // (G = 3: a few threads idle)
+  const int g = threadIdx.x % L / LPG, part = threadIdx.x % LPG, slot = threadIdx.x / L;
+  // Words of this thread that lie below head_dim.
+  const int words = min(K, (a.D - g * kGroup) / 8 - part * K);
+  const uint32_t quad = 0xFu << (lane_id() & 28u);
+  const int kv = blockIdx.z;
+  for (int bh = blockIdx.y; bh < a.B * a.H; bh += gridDim.y) {
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int64_t len = a.lens[b];
+    const int count = count_of(a, b, len);
     if (count < 0) {
-      if (p.kv == 0 && p.h == 0 && p.t == 0 && p.d0 == 0) atomicOr(a.err, kErrKvLength);
+      if (kv == 0 && h == 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrKvLength);
       continue;
     }
-    if (p.t >= count) continue;
-    const int64_t at = record_at(a, p.kv, p.b, p.h, len + p.t);
-    if (at < 0) {
-      if (p.kv == 0 && p.h == 0 && p.d0 == 0) atomicOr(a.err, kErrPage);
-      continue;
-    }
-    const int64_t* rs = a.rs[p.kv];
-    const uint16_t* src = a.rows[p.kv] + p.b * rs[0] + p.h * rs[1] + p.t * rs[2] + p.d0;
-    const bool live = p.d0 < a.D;  // head_dim is a multiple of 8
-    uint16_t v[8];
-    if (live) {
-      if (a.vec) {
-        *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src);
-      } else {
+    if (slot >= rows_per_block) continue;
+    const int64_t* rs = a.rs[kv];
+    const uint16_t* src = a.rows[kv] + b * rs[0] + h * rs[1] + g * kGroup + part * K * 8;
+    // (The threads of a group take the same branches.)
+    for (int t = blockIdx.x * rows_per_block + slot; t < count; t += gridDim.x * rows_per_block) {
+      uint32_t w[K][4];  // [eight values][packed pair]
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = src[i];
+      for (int k = 0; k < K; ++k) {
+        const uint16_t* from = src + t * rs[2] + 8 * k;
+        if (k >= words) {  // past head_dim: repeat, so that minimum and maximum hold
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[k][i] = k > 0 ? w[0][i] : 0u;
+        } else if (a.vec) {
+          const uint4 x = __ldcs(reinterpret_cast<const uint4*>(from));
+          w[k][0] = x.x;
+          w[k][1] = x.y;
+          w[k][2] = x.z;
+          w[k][3] = x.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[k][i] = from[2 * i] | (static_cast<uint32_t>(from[2 * i + 1]) << 16);
+        }
       }
-    }
-    float f[8];
-    float lo = INFINITY, hi = -INFINITY;
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = to_f32<F16>(v[i]);
-        lo = min_nan(lo, f[i]);
-        hi = max_nan(hi, f[i]);
+      const int64_t at = record_at(a, kv, b, h, len + t);
+      if (at < 0) {
+        if (kv == 0 && h == 0 && g == 0 && part == 0) atomicOr(a.err, kErrPage);
+        continue;
       }
-    }
+      uint32_t lo2 = w[0][0], hi2 = w[0][0];
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      lo = min_nan(lo, __shfl_xor_sync(quad, lo, o));
-      hi = max_nan(hi, __shfl_xor_sync(quad, hi, o));
-    }
-    // Not finite where the group holds a NaN or an infinity, or its spread overflows.
-    const float spread = __fsub_rn(hi, lo);
-    const bool finite = fabsf(spread) <= 3.402823466e38f;
-    const uint32_t s16 = finite ? to_16<F16>(__fdiv_rn(spread, 15.f)) : 0x7FFFu;
-    const uint32_t m16 = finite ? to_16<F16>(lo) : 0x7FFFu;
-    const float s = to_f32<F16>(s16);
-    uint32_t word = 0;
-    if (live && finite && s > 0.f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float c = fminf(rintf(__fdiv_rn(__fsub_rn(f[i], lo), s)), 15.f);
-        word |= static_cast<uint32_t>(c) << (4 * i);
+      for (int i = 1; i < 4 * K; ++i) {
+        lo2 = min2<F16>(lo2, w[i >> 2][i & 3]);
+        hi2 = max2<F16>(hi2, w[i >> 2][i & 3]);
       }
+      float lo = min_nan(to_f32<F16>(lo2 & 0xFFFFu), to_f32<F16>(lo2 >> 16));
+      float hi = max_nan(to_f32<F16>(hi2 & 0xFFFFu), to_f32<F16>(hi2 >> 16));
+      if (LPG > 1) {
+        if (words <= 0) {
+          lo = INFINITY;
+          hi = -INFINITY;
+        }
+#pragma unroll
+        for (int o = 1; o < LPG; o <<= 1) {
+          lo = min_nan(lo, __shfl_xor_sync(quad, lo, o));
+          hi = max_nan(hi, __shfl_xor_sync(quad, hi, o));
+        }
+      }
+      // Not finite where the group holds a NaN or an infinity, or its spread overflows.
+      const float spread = __fsub_rn(hi, lo);
+      const bool finite = fabsf(spread) <= 3.402823466e38f;
+      const uint32_t s16 = finite ? to_16<F16>(__fdiv_rn(spread, 15.f)) : 0x7FFFu;
+      const uint32_t m16 = finite ? to_16<F16>(lo) : 0x7FFFu;
+      const float s = to_f32<F16>(s16);
+      uint32_t code[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) code[k] = 0u;
+      if (finite && s > 0.f) {
+        if (s >= (F16 ? 6.103515625e-05f : 1.17549435e-38f)) {  // a normal number of the type
+          const float r = __frcp_rn(s), half = 0.5f * s;
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (k < words) code[k] = codes_of<F16>(w[k], lo, s, r, half);
+        } else {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (k < words) code[k] = codes_by_division<F16>(w[k], lo, s);
+        }
+      }
+      uint8_t* rec = a.cache[kv] + at;
+      if (LPG == 1)
+        *reinterpret_cast<uint4*>(rec + kHeadBytes + 16 * g) =
+            make_uint4(code[0], code[K / 4], code[K / 2], code[K - 1]);
+      else
+        *reinterpret_cast<uint32_t*>(rec + kHeadBytes + 16 * g + 4 * part) = code[0];
+      if (part == 0) *reinterpret_cast<uint32_t*>(rec + 4 * g) = s16 | (m16 << 16);
+      if (part == 0 && g == G - 1)  // the head's slots that no group has
+        for (int i = G; i < 4; ++i) *reinterpret_cast<uint32_t*>(rec + 4 * i) = 0u;
     }
-    uint8_t* rec = a.cache[p.kv] + at;
-    const int lane4 = (p.d0 >> 3) & 3;
-    *reinterpret_cast<uint32_t*>(rec + kHeadBytes + 16 * p.g + 4 * lane4) = word;
-    // The group's parameters, and zeros in the head's slots that no group has.
-    if (lane4 == 0) *reinterpret_cast<uint32_t*>(rec + 4 * p.g) = s16 | (m16 << 16);
-    if (p.g == 0 && lane4 >= G) *reinterpret_cast<uint32_t*>(rec + 4 * lane4) = 0u;
   }
   if (!a.advance) return;
 
@@ -149,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) gqa_q4_append_kernel(const Q4RowsArg
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1 ? 1 : 0;
+    last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y * gridDim.z - 1 ? 1 : 0;
   }
   __syncthreads();
   if (last) {
@@ -171,83 +260,137 @@ __global__ void __launch_bounds__(kThreads) gqa_q4_append_kernel(const Q4RowsArg
   }
 }
 
-template <bool F16>
-__global__ void __launch_bounds__(kThreads) gqa_q4_read_kernel(const Q4RowsArgs a,
-                                                               const uint32_t pieces) {
-  const int G = groups_of(a.D);
-  for (uint32_t x = blockIdx.x * kThreads + threadIdx.x; x < pieces; x += gridDim.x * kThreads) {
-    const Piece p = piece_of(x, a, G);
-    if (p.d0 >= a.D) continue;
-    const bool first = p.kv == 0 && p.h == 0 && p.t == 0 && p.d0 == 0;
+template <bool F16, int G, int kRows>
+__global__ void __launch_bounds__(kThreads) gqa_q4_read_kernel(const Q4RowsArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int L = 4 * G;
+  const int per_pass = blockDim.x / L;
+  const int piece = threadIdx.x % L, slot = threadIdx.x / L;
+  const int d0 = piece * 8, g = piece >> 2;
+  if (slot >= per_pass || d0 >= a.D) return;
+  const int kv = blockIdx.z;
+  for (int bh = blockIdx.y; bh < a.B * a.H; bh += gridDim.y) {
+    const int b = bh / a.H, h = bh - b * a.H;
+    const bool first = kv == 0 && h == 0 && blockIdx.x == 0 && threadIdx.x == 0;
     int64_t len = a.cap;
     if (a.lens != nullptr) {
-      len = a.lens[p.b];
+      len = a.lens[b];
       if (len < 0 || len > a.cap) {
         if (first) atomicOr(a.err, kErrKvLength);
         len = len < 0 ? 0 : a.cap;
       }
     }
-    const int64_t start = a.starts != nullptr ? a.starts[p.b] : a.start;
-    if (start < 0 && first) atomicOr(a.err, kErrKvLength);
-    const int64_t j = start + p.t;
-    uint32_t out[4] = {0u, 0u, 0u, 0u};
-    if (start >= 0 && j < len) {
-      const int64_t at = record_at(a, p.kv, p.b, p.h, j);
-      if (at < 0) {
-        if (p.kv == 0 && p.h == 0 && p.d0 == 0) atomicOr(a.err, kErrPage);
-      } else {
-        const uint8_t* rec = a.cache[p.kv] + at;
-        const uint32_t par = *reinterpret_cast<const uint32_t*>(rec + 4 * p.g);
-        const uint32_t word = *reinterpret_cast<const uint32_t*>(rec + kHeadBytes + p.d0 / 2);
-        const float s = scale_of<F16>(par), m = min_of<F16>(par);
+    const int64_t start = a.starts != nullptr ? a.starts[b] : a.start;
+    if (start < 0) {
+      if (first) atomicOr(a.err, kErrKvLength);
+      len = 0;
+    }
+    const int64_t* rs = a.rs[kv];
+    uint16_t* dst = a.rows[kv] + b * rs[0] + h * rs[1] + d0;
+    const int step = per_pass * kRows;
+    for (int t0 = blockIdx.x * step; t0 < a.n; t0 += gridDim.x * step) {
+      uint32_t par[kRows], word[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int t = t0 + k * per_pass + slot;
+        par[k] = word[k] = 0u;  // reads as zeros
+        if (t >= a.n || start + t >= len) continue;
+        const int64_t at = record_at(a, kv, b, h, start + t);
+        if (at < 0) {
+          if (kv == 0 && h == 0 && d0 == 0) atomicOr(a.err, kErrPage);
+          continue;
+        }
+        const uint8_t* rec = a.cache[kv] + at;
+        par[k] = *reinterpret_cast<const uint32_t*>(rec + 4 * g);
+        word[k] = *reinterpret_cast<const uint32_t*>(rec + kHeadBytes + d0 / 2);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int t = t0 + k * per_pass + slot;
+        if (t >= a.n) continue;
+        const float s = scale_of<F16>(par[k]), m = min_of<F16>(par[k]);
+        uint32_t out[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          out[i] = pack2<F16>(fmaf(s, static_cast<float>((word >> (8 * i)) & 15u), m),
-                              fmaf(s, static_cast<float>((word >> (8 * i + 4)) & 15u), m));
-      }
-    }
-    const int64_t* rs = a.rs[p.kv];
-    uint16_t* dst = a.rows[p.kv] + p.b * rs[0] + p.h * rs[1] + p.t * rs[2] + p.d0;
-    if (a.vec) {
-      *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    } else {
+          out[i] = pack2<F16>(fmaf(s, static_cast<float>((word[k] >> (8 * i)) & 15u), m),
+                              fmaf(s, static_cast<float>((word[k] >> (8 * i + 4)) & 15u), m));
+        uint16_t* to = dst + t * rs[2];
+        if (a.vec) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(out[0], out[1], out[2], out[3]);
+        } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dst[2 * i] = static_cast<uint16_t>(out[i] & 0xFFFFu);
-        dst[2 * i + 1] = static_cast<uint16_t>(out[i] >> 16);
+          for (int i = 0; i < 4; ++i) {
+            to[2 * i] = static_cast<uint16_t>(out[i] & 0xFFFFu);
+            to[2 * i + 1] = static_cast<uint16_t>(out[i] >> 16);
+          }
+        }
       }
     }
   }
 }
 
-uint32_t pieces_of(const Q4RowsArgs& a) {
-  return 2u * static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.H) *
-         static_cast<uint32_t>(a.n) * 4u * static_cast<uint32_t>(groups_of(a.D));
+template <typename Kernel>
+int launch_rows(Kernel kern, const Q4RowsArgs& a, int per_row, int rows, cudaStream_t stream) {
+  // per_row threads for a row, `rows` rows in turn per thread; blocks of as
+  // many threads as a short run of rows has work for.
+  const int64_t want = (static_cast<int64_t>(a.n) * per_row + 31) / 32 * 32;
+  const int threads = want < kThreads ? static_cast<int>(want) : kThreads;
+  const int64_t step = static_cast<int64_t>(threads / per_row) * rows;
+  const int64_t bh = static_cast<int64_t>(a.B) * a.H;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.n + step - 1) / step),
+                     static_cast<unsigned>(bh < 32768 ? bh : 32768), 2);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) {
+    cudaGetLastError();
+    return GQA_ERR_CUDA;
+  }
+  return GQA_OK;
 }
 
-unsigned grid_of(uint32_t pieces) {
-  const uint32_t blocks = (pieces + kThreads - 1) / kThreads;
-  return blocks < 148u * 32u ? blocks : 148u * 32u;
+// Whether there are several eight-value pieces for every thread that fits the
+// machine: then a thread takes several of them; fewer are spread wide.
+bool many_rows(const Q4RowsArgs& a, int G) {
+  return 2.0 * a.B * a.H * a.n * 4 * G >= kManyPieces;
+}
+
+template <bool F16, int G>
+int append_g(const Q4RowsArgs& a, cudaStream_t stream) {
+  return many_rows(a, G) ? launch_rows(gqa_q4_append_kernel<F16, G, 1>, a, G, 1, stream)
+                         : launch_rows(gqa_q4_append_kernel<F16, G, 4>, a, 4 * G, 1, stream);
+}
+
+template <bool F16, int G>
+int read_g(const Q4RowsArgs& a, cudaStream_t stream) {
+  return many_rows(a, G) ? launch_rows(gqa_q4_read_kernel<F16, G, 4>, a, 4 * G, 4, stream)
+                         : launch_rows(gqa_q4_read_kernel<F16, G, 1>, a, 4 * G, 1, stream);
 }
 
 }  // namespace
 
 int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream) {
-  const uint32_t pieces = pieces_of(a);
-  if (f16)
-    gqa_q4_append_kernel<true><<<grid_of(pieces), kThreads, 0, stream>>>(a, pieces);
-  else
-    gqa_q4_append_kernel<false><<<grid_of(pieces), kThreads, 0, stream>>>(a, pieces);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+  switch (groups_of(a.D)) {
+    case 1: return f16 ? append_g<true, 1>(a, stream) : append_g<false, 1>(a, stream);
+    case 2: return f16 ? append_g<true, 2>(a, stream) : append_g<false, 2>(a, stream);
+    case 3: return f16 ? append_g<true, 3>(a, stream) : append_g<false, 3>(a, stream);
+    default: return f16 ? append_g<true, 4>(a, stream) : append_g<false, 4>(a, stream);
+  }
 }
 
 int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream) {
-  const uint32_t pieces = pieces_of(a);
-  if (f16)
-    gqa_q4_read_kernel<true><<<grid_of(pieces), kThreads, 0, stream>>>(a, pieces);
-  else
-    gqa_q4_read_kernel<false><<<grid_of(pieces), kThreads, 0, stream>>>(a, pieces);
-  return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+  switch (groups_of(a.D)) {
+    case 1: return f16 ? read_g<true, 1>(a, stream) : read_g<false, 1>(a, stream);
+    case 2: return f16 ? read_g<true, 2>(a, stream) : read_g<false, 2>(a, stream);
+    case 3: return f16 ? read_g<true, 3>(a, stream) : read_g<false, 3>(a, stream);
+    default: return f16 ? read_g<true, 4>(a, stream) : read_g<false, 4>(a, stream);
+  }
 }
 
 }  // namespace gqa

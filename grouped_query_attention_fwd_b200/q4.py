@@ -48,18 +48,35 @@ _lib.gqa_forward_q4.argtypes = [ctypes.POINTER(Problem), _vp, _vp, _vp, _vp, _vp
                                 ctypes.c_size_t, _vp]
 _lib.gqa_forward_q4.restype = ctypes.c_int
 
-# Checked descriptors by sizes, strides and scalars (never by address), per
-# thread: a call writes its pointers into the descriptor it uses.
+# Checked descriptors, per thread (a call writes its pointers into the one it
+# uses).  The key is everything that the checks look at: types, devices, sizes,
+# strides and scalars of every argument, never an address.
 _seen = threading.local()
 _MAX_SEEN = 1024
 
 
-def _remember(kind, key, value):
-    seen = getattr(_seen, kind)
+def _known(kind):
+    seen = getattr(_seen, kind, None)
+    if seen is None:
+        seen = {}
+        setattr(_seen, kind, seen)
+    return seen
+
+
+def _remember(seen, key, value):
     if len(seen) >= _MAX_SEEN:
         seen.clear()
     seen[key] = value
     return value
+
+
+def _like(t):
+    """What the checks see of a tensor (or None)."""
+    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def q4_record_bytes(head_dim: int) -> int:
@@ -88,33 +105,33 @@ def _check_caches(cache_k, cache_v):
         raise ValueError("the K and V caches must have one shape")
 
 
-def _device_of(first, *others) -> int:
-    """Index of the CUDA device that all tensors (or None) are on."""
-    idx = first.get_device()
+def _check_devices(idx, *tensors):
     if idx < 0:
         raise ValueError("the 4-bit cache takes CUDA tensors only (there is no CPU path)")
-    for t in others:
+    for t in tensors:
         if t is not None and t.get_device() != idx:
             raise ValueError("all tensors must be on the same CUDA device")
-    return idx
 
 
-def _contexts(idx, stream):
-    """What a call has to enter so that its device and its stream are current:
-    nothing, mostly."""
+def _elsewhere(idx, stream):
+    """Contexts that make device ``idx`` and ``stream`` current, or None where
+    they are (the usual case)."""
+    c = _torch()._C
+    if idx < 0 or (c._cuda_getDevice() == idx and
+                   (stream is None or int(stream) == c._cuda_getCurrentRawStream(idx))):
+        return None
     torch = _torch()
-    got = []
-    if torch._C._cuda_getDevice() != idx:
-        got.append(torch.cuda.device(idx))
-    if stream is not None and int(stream) != torch._C._cuda_getCurrentRawStream(idx):
-        got.append(torch.cuda.stream(_stream_object(idx, stream)))
-    return got
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(idx))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(_stream_object(idx, stream)))
+    return stack
 
 
 _HEAD = 256 + 65536  # error word, append ticket and decode tickets: what has to start at zero
 
 
-def _workspace(idx, nbytes, workspace):
+def _workspace(idx, stream, nbytes, workspace):
     """The caller's workspace, the cached one of the current stream, or, in a
     capture, one that belongs to the graph alone (zeroed by each replay):
     graphs replayed side by side never share one."""
@@ -125,22 +142,10 @@ def _workspace(idx, nbytes, workspace):
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
         ws[:_HEAD].zero_()
         return ws
-    stream = torch._C._cuda_getCurrentRawStream(idx)
     ws = _workspaces.get((idx, stream))
     if ws is None or ws.numel() < nbytes:
         ws = workspace_for(torch.device("cuda", idx), nbytes, stream)
     return ws
-
-
-def _enter(idx, stream, call, *args):
-    """call(stream handle, *args) with the device and the stream current."""
-    contexts = _contexts(idx, stream)
-    if not contexts:
-        return call(_torch()._C._cuda_getCurrentRawStream(idx), *args)
-    with contextlib.ExitStack() as stack:
-        for c in contexts:
-            stack.enter_context(c)
-        return call(_torch()._C._cuda_getCurrentRawStream(idx), *args)
 
 
 # ------------------------------------------------------------ append and read back
@@ -169,11 +174,10 @@ def _rows_desc(dtype, cache_k, cache_v, k, v, D, table, advance):
     return d
 
 
-def _int32(t, B, name):
-    torch = _torch()
-    if t.dtype is not torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous():
+def _check_int32(t, B, name):
+    if t is not None and (t.dtype is not _torch().int32 or tuple(t.shape) != (B,) or
+                          not t.is_contiguous()):
         raise ValueError("%s must be a contiguous int32 CUDA tensor of shape [B]" % name)
-    return t.data_ptr()
 
 
 def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance=True,
@@ -187,29 +191,35 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
     False leaves it, for layers that share one tensor of lengths.  An entry
     that does not fit is left as it was and device_status() reports
     GQA_ERR_KV_LENGTH."""
-    idx = _device_of(k_new, v_new, kv_lens, cache_k, cache_v, new_lens, block_table)
-    _check_caches(cache_k, cache_v)
-    if k_new.dim() != 4 or v_new.dtype is not k_new.dtype:
-        raise TypeError("k_new and v_new must be [B, Hkv, n, D] of one type")
-    B = k_new.shape[0]
-    bt = _table(block_table, B)[0] if block_table is not None else None
-    key = (k_new.dtype, k_new.shape, k_new.stride(), v_new.shape, v_new.stride(), cache_k.shape,
-           cache_k.stride(), cache_v.stride(), advance,
-           None if bt is None else (block_table.shape, block_table.stride(0)))
-    d = _seen.__dict__.setdefault("append", {}).get(key)
+    idx = k_new.get_device()
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens, advance,
+                                workspace, None, block_table)
+    key = (_like(k_new), _like(v_new), _like(cache_k), _like(cache_v), _like(kv_lens),
+           _like(new_lens), _like(block_table), advance)
+    seen = _known("append")
+    d = seen.get(key)
     if d is None:
-        d = _remember("append", key, _rows_desc(k_new.dtype, cache_k, cache_v, k_new, v_new,
-                                                k_new.shape[3], block_table, bool(advance)))
-    d.block_table = bt
-    d.counts = None if new_lens is None else _int32(new_lens, B, "new_lens")
-    lens = _int32(kv_lens, B, "kv_lens")
-
-    def call(handle):
-        ws = _workspace(idx, 256, workspace)
-        return _lib.gqa_kv_append_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k_new.data_ptr(),
-                                     v_new.data_ptr(), lens, ws.data_ptr(), ws.numel(), handle)
-
-    rc = _enter(idx, stream, call)
+        _check_devices(idx, v_new, kv_lens, cache_k, cache_v, new_lens, block_table)
+        _check_caches(cache_k, cache_v)
+        if k_new.dim() != 4 or v_new.dtype is not k_new.dtype:
+            raise TypeError("k_new and v_new must be [B, Hkv, n, D] of one type")
+        B = k_new.shape[0]
+        if block_table is not None:
+            _table(block_table, B)
+        _check_int32(new_lens, B, "new_lens")
+        _check_int32(kv_lens, B, "kv_lens")
+        d = _remember(seen, key, _rows_desc(k_new.dtype, cache_k, cache_v, k_new, v_new,
+                                            k_new.shape[3], block_table, bool(advance)))
+    d.block_table = _ptr(block_table)
+    d.counts = _ptr(new_lens)
+    handle = _torch()._C._cuda_getCurrentRawStream(idx)
+    ws = _workspace(idx, handle, 256, workspace)
+    rc = _lib.gqa_kv_append_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k_new.data_ptr(),
+                               v_new.data_ptr(), kv_lens.data_ptr(), ws.data_ptr(), ws.numel(),
+                               handle)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_kv_append_q4")
 
@@ -222,43 +232,49 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
     int, or an int32 CUDA tensor [B].  n defaults to the rest of the capacity.
     Rows at or past kv_lens[b] (the capacity without it) are zeros."""
     torch = _torch()
+    idx = cache_k.get_device()
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens, start, n, out_k, out_v,
+                              workspace, None, block_table)
     starts = start if isinstance(start, torch.Tensor) else None
-    idx = _device_of(cache_k, cache_v, kv_lens, starts, out_k, out_v, block_table)
-    _check_caches(cache_k, cache_v)
-    B, Hkv, capacity, _ = cache_k.shape
-    bt = None
-    if block_table is not None:
-        B = block_table.shape[0]
-        bt = _table(block_table, B)[0]
-        capacity *= block_table.shape[1]
-    if n is None:
-        n = capacity - (0 if starts is not None else int(start))
-    if n < 0:
-        raise ValueError("n must not be negative")
-    shape = (B, Hkv, int(n), int(head_dim))
-    for t in (out_k, out_v):
-        if t is not None and (t.shape != shape or t.dtype is not dtype):
-            raise ValueError("out_k and out_v must be [B, Hkv, n, D] of the given type")
-
-    def call(handle):
-        k = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_k is None else out_k
-        v = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_v is None else out_v
-        key = (dtype, shape, k.stride(), v.stride(), cache_k.shape, cache_k.stride(),
-               cache_v.stride(), None if bt is None else (block_table.shape, block_table.stride(0)))
-        d = _seen.__dict__.setdefault("read", {}).get(key)
-        if d is None:
-            d = _remember("read", key, _rows_desc(dtype, cache_k, cache_v, k, v, shape[3],
-                                                  block_table, False))
-        d.block_table = bt
-        d.starts = None if starts is None else _int32(starts, B, "start")
-        d.start = 0 if starts is not None else int(start)
-        lens = None if kv_lens is None else _int32(kv_lens, B, "kv_lens")
-        ws = _workspace(idx, 256, workspace)
-        rc = _lib.gqa_kv_read_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k.data_ptr(),
-                                 v.data_ptr(), lens, ws.data_ptr(), ws.numel(), handle)
-        return rc, k, v
-
-    rc, k, v = _enter(idx, stream, call)
+    start = 0 if starts is not None else int(start)
+    key = (dtype, head_dim, n, start if n is None else None, _like(cache_k), _like(cache_v),
+           _like(kv_lens), _like(starts), _like(out_k), _like(out_v), _like(block_table))
+    seen = _known("read")
+    known = seen.get(key)
+    if known is None:
+        _check_devices(idx, cache_v, kv_lens, starts, out_k, out_v, block_table)
+        _check_caches(cache_k, cache_v)
+        B, Hkv, capacity, _ = cache_k.shape
+        if block_table is not None:
+            B = block_table.shape[0]
+            _table(block_table, B)
+            capacity *= block_table.shape[1]
+        _check_int32(starts, B, "start")
+        _check_int32(kv_lens, B, "kv_lens")
+        count = int(n) if n is not None else capacity - start
+        if count < 0:
+            raise ValueError("n must not be negative")
+        shape = (B, Hkv, count, int(head_dim))
+        for t in (out_k, out_v):
+            if t is not None and (t.shape != shape or t.dtype is not dtype):
+                raise ValueError("out_k and out_v must be [B, Hkv, n, D] of the given type")
+        fresh = torch.empty(shape, dtype=dtype, device="meta")
+        known = _remember(seen, key, (shape, _rows_desc(
+            dtype, cache_k, cache_v, fresh if out_k is None else out_k,
+            fresh if out_v is None else out_v, shape[3], block_table, False)))
+    shape, d = known
+    k = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_k is None else out_k
+    v = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_v is None else out_v
+    d.block_table = _ptr(block_table)
+    d.starts = _ptr(starts)
+    d.start = start
+    handle = torch._C._cuda_getCurrentRawStream(idx)
+    ws = _workspace(idx, handle, 256, workspace)
+    rc = _lib.gqa_kv_read_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k.data_ptr(),
+                             v.data_ptr(), _ptr(kv_lens), ws.data_ptr(), ws.numel(), handle)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_kv_read_q4")
     return k, v
@@ -327,36 +343,34 @@ def forward_q4(q, cache_k, cache_v, mask=None, causal=False, scale=None, out=Non
     q and the result are bf16 or fp16, the type the cache was written with;
     every other argument is ``forward``'s."""
     torch = _torch()
-    idx = _device_of(q, cache_k, cache_v, mask, kv_lens, block_table, out)
-    _check_caches(cache_k, cache_v)
-    if mask is not None:
-        if mask.dtype is torch.bool:
-            mask = mask.view(torch.uint8)
-        elif mask.dtype is not torch.uint8:
+    idx = q.get_device()
+    away = _elsewhere(idx, stream)
+    if away is not None:
+        with away:
+            return forward_q4(q, cache_k, cache_v, mask, causal, scale, out, workspace, None,
+                              causal_offset, window, kv_lens, block_table)
+    key = (_like(q), _like(cache_k), _like(cache_v), _like(mask), _like(kv_lens),
+           _like(block_table), _like(out), causal, scale, causal_offset, window)
+    seen = _known("forward")
+    known = seen.get(key)
+    if known is None:
+        _check_devices(idx, cache_k, cache_v, mask, kv_lens, block_table, out)
+        _check_caches(cache_k, cache_v)
+        if mask is not None and mask.dtype not in (torch.bool, torch.uint8):
             raise TypeError("mask must be bool or uint8")
-
-    def call(handle, o):
-        if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        key = (q.dtype, q.shape, q.stride(), o.shape, o.dtype, o.stride(), cache_k.shape,
-               cache_k.stride(), cache_v.stride(),
-               None if mask is None else (mask.shape, mask.stride()), causal, scale,
-               causal_offset, window, kv_lens is None, idx,
-               None if block_table is None else (block_table.shape, block_table.stride(0)))
-        known = _seen.__dict__.setdefault("forward", {}).get(key)
-        if known is None:
-            p = q4_problem_for(q, cache_k, cache_v, mask, causal, scale, o, causal_offset,
-                               window, kv_lens, block_table)
-            known = _remember("forward", key, (p, _query(p).workspace_bytes))
-        p, nbytes = known
-        p.kv_lens = None if kv_lens is None else _int32(kv_lens, q.shape[0], "kv_lens")
-        p.block_table = None if block_table is None else _table(block_table, q.shape[0])[0]
-        ws = _workspace(idx, nbytes, workspace)
-        return _lib.gqa_forward_q4(p, q.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(),
-                                   mask.data_ptr() if mask is not None else None, o.data_ptr(),
-                                   ws.data_ptr(), ws.numel(), handle), o
-
-    rc, out = _enter(idx, stream, call, out)
+        _check_int32(kv_lens, q.shape[0], "kv_lens")
+        p = q4_problem_for(q, cache_k, cache_v, mask, causal, scale, out, causal_offset, window,
+                           kv_lens, block_table)
+        known = _remember(seen, key, (p, _query(p).workspace_bytes))
+    p, nbytes = known
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    p.kv_lens = _ptr(kv_lens)
+    p.block_table = _ptr(block_table)
+    handle = torch._C._cuda_getCurrentRawStream(idx)
+    ws = _workspace(idx, handle, nbytes, workspace)
+    rc = _lib.gqa_forward_q4(p, q.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), _ptr(mask),
+                             out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
     if rc != GQA_OK:
         raise GQAError(rc, "gqa_forward_q4")
     return out
