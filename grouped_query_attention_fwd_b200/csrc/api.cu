@@ -293,6 +293,58 @@ int encode_decode_kv_map(CUtensorMap* map, const void* base, const gqa_problem& 
   return encode_half_map(map, base, p.batch, p.heads_kv, p.seq_k, p.head_dim, st,
                          kDecodeKeysPerTile, 1, f16);
 }
+
+// Prefill of a validated problem: tensor maps, arguments and launches.
+int launch_prefill_call(const gqa_problem& p, int sms, const void* q, const void* k, const void* v,
+                        const uint8_t* mask, void* out, uint8_t* ws, cudaStream_t stream) {
+  uint32_t* err = reinterpret_cast<uint32_t*>(ws);
+  const float scale_log2 =
+      static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634073599);
+  const int64_t g = p.heads_q / p.heads_kv;
+  const PrefillShape s = plan_prefill(p, sms);
+  CUtensorMap tmq, tmk, tmv;
+  const bool f16 = p.dtype == GQA_DTYPE_F16;
+  int erc = encode_half_map(&tmq, q, p.batch, p.heads_q, p.seq_q, p.head_dim, p.q_stride,
+                            static_cast<uint32_t>(s.qpt), static_cast<uint32_t>(g), f16);
+  if (erc != GQA_OK) return erc;
+  if (p.block_table != nullptr) {  // paged: 64-key boxes, one page each
+    erc = encode_decode_kv_map(&tmk, k, p, p.k_stride);
+    if (erc != GQA_OK) return erc;
+    erc = encode_decode_kv_map(&tmv, v, p, p.v_stride);
+    if (erc != GQA_OK) return erc;
+  } else {
+    erc = encode_half_map(&tmk, k, p.batch, p.heads_kv, p.seq_k, p.head_dim, p.k_stride, 128,
+                          1, f16);
+    if (erc != GQA_OK) return erc;
+    erc = encode_half_map(&tmv, v, p.batch, p.heads_kv, p.seq_k, p.head_dim, p.v_stride, 128,
+                          1, f16);
+    if (erc != GQA_OK) return erc;
+  }
+  PrefillArgs a{};
+  a.mask = p.has_mask ? mask : nullptr;
+  for (int d = 0; d < 3; ++d) a.ms[d] = p.mask_stride[d];
+  a.out = static_cast<uint16_t*>(out);
+  for (int d = 0; d < 4; ++d) a.os[d] = p.o_stride[d];
+  a.summary = ws + s.summary_offset;
+  a.order = s.order_offset >= 0 ? reinterpret_cast<int32_t*>(ws + s.order_offset) : nullptr;
+  a.bounds = s.bounds_offset >= 0 ? reinterpret_cast<int32_t*>(ws + s.bounds_offset) : nullptr;
+  a.err = err;
+  a.B = static_cast<int>(p.batch);
+  a.Hq = static_cast<int>(p.heads_q);
+  a.Hkv = static_cast<int>(p.heads_kv);
+  a.Sq = static_cast<int>(p.seq_q);
+  a.Sk = static_cast<int>(p.seq_k);
+  a.g = static_cast<int>(g);
+  a.causal = p.causal;
+  a.causal_offset = p.causal_offset;
+  a.window = p.window;
+  a.has_mask = p.has_mask;
+  a.lens = p.kv_lens;
+  a.Dv = static_cast<int>(p.head_dim);
+  a.scale_log2 = scale_log2;
+  if (s.pp) return launch_prefill_pp(p, s, a, tmq, tmk, tmv, stream);
+  return launch_prefill(p, s, a, tmq, tmk, tmv, stream);
+}
 }  // namespace gqa
 
 using namespace gqa;
@@ -367,9 +419,6 @@ GQA_API int gqa_forward(const gqa_problem* pp, const void* q, const void* k, con
 
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
     return GQA_ERR_LAYOUT;
-  const float scale_log2 =
-      static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634073599);
-  const int64_t g = p.heads_q / p.heads_kv;
 
   if (plan.kernel == GQA_KERNEL_DECODE) {
     const DecodeShape s = plan_decode(p, sms);
@@ -388,50 +437,7 @@ GQA_API int gqa_forward(const gqa_problem* pp, const void* q, const void* k, con
     return launch_decode(p, s, a, tmk, tmv, stream);
   }
 
-  // Prefill.
-  const PrefillShape s = plan_prefill(p, sms);
-  CUtensorMap tmq, tmk, tmv;
-  const bool f16 = p.dtype == GQA_DTYPE_F16;
-  int erc = encode_half_map(&tmq, q, p.batch, p.heads_q, p.seq_q, p.head_dim, p.q_stride,
-                            static_cast<uint32_t>(s.qpt), static_cast<uint32_t>(g), f16);
-  if (erc != GQA_OK) return erc;
-  if (p.block_table != nullptr) {  // paged: 64-key boxes, one page each
-    erc = encode_decode_kv_map(&tmk, k, p, p.k_stride);
-    if (erc != GQA_OK) return erc;
-    erc = encode_decode_kv_map(&tmv, v, p, p.v_stride);
-    if (erc != GQA_OK) return erc;
-  } else {
-    erc = encode_half_map(&tmk, k, p.batch, p.heads_kv, p.seq_k, p.head_dim, p.k_stride, 128,
-                          1, f16);
-    if (erc != GQA_OK) return erc;
-    erc = encode_half_map(&tmv, v, p.batch, p.heads_kv, p.seq_k, p.head_dim, p.v_stride, 128,
-                          1, f16);
-    if (erc != GQA_OK) return erc;
-  }
-  PrefillArgs a{};
-  a.mask = p.has_mask ? mask : nullptr;
-  for (int d = 0; d < 3; ++d) a.ms[d] = p.mask_stride[d];
-  a.out = static_cast<uint16_t*>(out);
-  for (int d = 0; d < 4; ++d) a.os[d] = p.o_stride[d];
-  a.summary = ws + s.summary_offset;
-  a.order = s.order_offset >= 0 ? reinterpret_cast<int32_t*>(ws + s.order_offset) : nullptr;
-  a.bounds = s.bounds_offset >= 0 ? reinterpret_cast<int32_t*>(ws + s.bounds_offset) : nullptr;
-  a.err = err;
-  a.B = static_cast<int>(p.batch);
-  a.Hq = static_cast<int>(p.heads_q);
-  a.Hkv = static_cast<int>(p.heads_kv);
-  a.Sq = static_cast<int>(p.seq_q);
-  a.Sk = static_cast<int>(p.seq_k);
-  a.g = static_cast<int>(g);
-  a.causal = p.causal;
-  a.causal_offset = p.causal_offset;
-  a.window = p.window;
-  a.has_mask = p.has_mask;
-  a.lens = p.kv_lens;
-  a.Dv = static_cast<int>(p.head_dim);
-  a.scale_log2 = scale_log2;
-  if (s.pp) return launch_prefill_pp(p, s, a, tmq, tmk, tmv, stream);
-  return launch_prefill(p, s, a, tmq, tmk, tmv, stream);
+  return launch_prefill_call(p, sms, q, k, v, mask, out, ws, stream);
 }
 
 GQA_API int gqa_kv_append(const gqa_kv_append_desc* d, void* cache_k, void* cache_v,

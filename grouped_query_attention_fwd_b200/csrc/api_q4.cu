@@ -13,6 +13,13 @@ namespace {
 
 constexpr int64_t kLim = int64_t(1) << 31;
 
+// Times that the choice between the two ways of attending goes by (ns, this
+// library's kernels): launch and ends of a decode, a 128-key unit of one SM at
+// up to 8 and up to 16 rows; a slice's launches and ends, a key tile of the
+// two-tile prefill; bytes read and written by the read back.
+constexpr double kDecodeNs = 10000, kUnitNs = 600, kUnit2Ns = 1200;
+constexpr double kSliceNs = 12000, kTwoTileNs = 2200, kReadBytesPerNs = 4500;
+
 bool aligned(const void* ptr, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
 }
@@ -43,8 +50,87 @@ int validate_q4(const gqa_problem* pp) {
   return GQA_OK;
 }
 
+// The way over 16-bit scratch for long query blocks: entries (whole, or some
+// of one's kv heads) in slices whose keys and values are read back, then
+// attended to by the prefill kernels.
+struct SlicePlan {
+  int64_t nb, nh;            // entries and kv heads per slice (nb > 1 only with every head)
+  int64_t head_bytes;        // scratch of one kv head's K (or V)
+  int64_t k_offset, v_offset, workspace_end;
+  int64_t slices;
+  int launches;
+  double ns;                 // estimated time
+};
+
+// The problem of a slice: nb entries from b0, nh kv heads from h0, contiguous
+// 16-bit K and V.
+gqa_problem slice_problem(const gqa_problem& p, int64_t b0, int64_t nb, int64_t nh) {
+  gqa_problem c = p;
+  const int64_t D = p.head_dim, S = p.seq_k;
+  c.batch = nb;
+  c.heads_kv = nh;
+  c.heads_q = nh * (p.heads_q / p.heads_kv);
+  const int64_t st[4] = {nh * S * D, S * D, D, 1};
+  for (int i = 0; i < 4; ++i) c.k_stride[i] = c.v_stride[i] = st[i];
+  if (p.kv_lens != nullptr) c.kv_lens = p.kv_lens + b0;
+  c.block_table = nullptr;
+  c.block_table_stride = c.page_size = c.num_pages = 0;
+  return c;
+}
+
+constexpr int64_t kSliceL2 = int64_t(64) << 20;     // scratch that stays in L2 beside the rest
+constexpr int64_t kSliceMost = int64_t(1) << 30;    // scratch of a slice, unless one head needs more
+
+SlicePlan plan_slices(const gqa_problem& p, int sms) {
+  SlicePlan s{};
+  const int64_t g = p.heads_q / p.heads_kv;
+  s.head_bytes = (p.seq_k * p.head_dim * 2 + 255) / 256 * 256;
+  const int64_t qpt = 128 / g;
+  const int64_t items = ((p.seq_q + qpt - 1) / qpt + 1) / 2;  // two-tile work items per kv head
+  // Enough heads for two rounds of items over the SMs, or more while the
+  // scratch stays in L2.
+  int64_t heads = (2 * sms + items - 1) / items;
+  const int64_t fit = kSliceL2 / (2 * s.head_bytes);
+  if (heads < fit) heads = fit;
+  const int64_t most = kSliceMost / (2 * s.head_bytes);
+  if (heads > most) heads = most;
+  if (heads < 1) heads = 1;
+  if (heads >= p.heads_kv) {
+    s.nh = p.heads_kv;
+    s.nb = heads / p.heads_kv < p.batch ? heads / p.heads_kv : p.batch;
+  } else {
+    s.nb = 1;
+    s.nh = heads;
+  }
+  const gqa_problem c = slice_problem(p, 0, s.nb, s.nh);
+  const PrefillShape f = plan_prefill(c, sms);
+  s.k_offset = (f.workspace_end + 255) / 256 * 256;
+  s.v_offset = s.k_offset + s.nb * s.nh * s.head_bytes;
+  s.workspace_end = s.v_offset + s.nb * s.nh * s.head_bytes;
+  s.slices = (p.batch + s.nb - 1) / s.nb * ((p.heads_kv + s.nh - 1) / s.nh);
+  s.launches = static_cast<int>(s.slices) *
+               (2 + (p.has_mask ? 1 : 0) + (f.order_offset >= 0 ? 1 : 0));
+  const double rounds = double((s.nb * s.nh * items + sms - 1) / sms);
+  const double bytes = 2.0 * double(p.batch * p.heads_kv) *
+                       double(p.seq_k * (q4::record_bytes(static_cast<int>(p.head_dim)) +
+                                         2 * p.head_dim));
+  s.ns = double(s.slices) * (kSliceNs + rounds * double((p.seq_k + 127) / 128) * kTwoTileNs) +
+         bytes / kReadBytesPerNs;
+  return s;
+}
+
+// Estimated time of the decode kernel over the same problem.
+double decode_ns(const DecodeShape& s, int sms) {
+  return kDecodeNs + double(s.units) / sms * (s.NT == 1 ? kUnitNs : kUnit2Ns);
+}
+
+// Query blocks of up to 16 rows per kv head take one pass over the records;
+// longer ones take a pass per 16 rows, or go over 16-bit scratch.
+bool use_slices(const gqa_problem& p, const DecodeShape& d, const SlicePlan& s, int sms) {
+  return d.passes > 1 && p.seq_q > 1 && s.ns < decode_ns(d, sms);
+}
+
 int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
-  (void)sm_count;
   std::memset(plan, 0, sizeof(*plan));
   const int64_t qo = p.batch * p.heads_q * p.seq_q * p.head_dim * 2;
   const int64_t kv = p.batch * p.heads_kv * p.seq_k * q4::record_bytes(static_cast<int>(p.head_dim));
@@ -54,21 +140,86 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
   plan->workspace_bytes = kWorkspaceHeadBytes;
   if (p.batch == 0 || p.seq_q == 0) {
     plan->kernel = GQA_KERNEL_NONE;
-  } else if (p.seq_k == 0 || nothing_visible(p)) {
+    return GQA_OK;
+  }
+  if (p.seq_k == 0 || nothing_visible(p)) {
     plan->kernel = p.seq_k == 0 ? GQA_KERNEL_ZERO : GQA_KERNEL_NAN;
     plan->grid = 592;
     plan->block = 256;
     plan->launches = 1;
-  } else {
-    const DecodeShape s = plan_decode_q4(p, sm_count);
-    if (s.units >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit unit indices
-    plan->kernel = GQA_KERNEL_Q4;
-    plan->grid = s.grid;
-    plan->block = decode_q4_threads(s);
-    plan->smem_bytes = s.smem_bytes;
-    plan->launches = s.zero_counters ? 2 : 1;
-    plan->work_units = static_cast<int32_t>(s.units);
-    plan->workspace_bytes = (s.workspace_end + 255) / 256 * 256;
+    return GQA_OK;
+  }
+  const DecodeShape s = plan_decode_q4(p, sm_count);
+  const SlicePlan sl = plan_slices(p, sm_count);
+  if (use_slices(p, s, sl, sm_count)) {
+    const PrefillShape f = plan_prefill(slice_problem(p, 0, sl.nb, sl.nh), sm_count);
+    plan->kernel = GQA_KERNEL_Q4_PREFILL;
+    plan->grid = f.grid;
+    plan->block = kPrefillThreads;
+    plan->smem_bytes = f.smem_bytes;
+    plan->launches = sl.launches;
+    plan->work_units = static_cast<int32_t>(f.work * sl.slices);
+    plan->workspace_bytes = (sl.workspace_end + 255) / 256 * 256;
+    return GQA_OK;
+  }
+  if (s.units >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit unit indices
+  plan->kernel = GQA_KERNEL_Q4;
+  plan->grid = s.grid;
+  plan->block = decode_q4_threads(s);
+  plan->smem_bytes = s.smem_bytes;
+  plan->launches = s.zero_counters ? 2 : 1;
+  plan->work_units = static_cast<int32_t>(s.units);
+  plan->workspace_bytes = (s.workspace_end + 255) / 256 * 256;
+  return GQA_OK;
+}
+
+int run_slices(const gqa_problem& p, const SlicePlan& s, int sms, const void* q,
+               const uint8_t* ck, const uint8_t* cv, const uint8_t* mask, void* out, uint8_t* ws,
+               cudaStream_t stream) {
+  const bool f16 = p.dtype == GQA_DTYPE_F16;
+  const int64_t g = p.heads_q / p.heads_kv;
+  const bool paged = p.block_table != nullptr;
+  for (int64_t b0 = 0; b0 < p.batch; b0 += s.nb) {
+    for (int64_t h0 = 0; h0 < p.heads_kv; h0 += s.nh) {
+      const int64_t nb = p.batch - b0 < s.nb ? p.batch - b0 : s.nb;
+      const int64_t nh = p.heads_kv - h0 < s.nh ? p.heads_kv - h0 : s.nh;
+      const gqa_problem c = slice_problem(p, b0, nb, nh);
+      Q4RowsArgs a{};
+      const uint8_t* caches[2] = {ck, cv};
+      const int64_t* strides[2] = {p.k_stride, p.v_stride};
+      const int64_t offsets[2] = {s.k_offset, s.v_offset};
+      for (int i = 0; i < 2; ++i) {
+        a.cache[i] = const_cast<uint8_t*>(caches[i]) + h0 * strides[i][1] +
+                     (paged ? 0 : b0 * strides[i][0]);
+        a.rows[i] = reinterpret_cast<uint16_t*>(ws + offsets[i]);
+        for (int d = 0; d < 3; ++d) {
+          a.cs[i][d] = strides[i][d];
+          a.rs[i][d] = c.k_stride[d];
+        }
+      }
+      a.lens = const_cast<int32_t*>(c.kv_lens);
+      a.err = reinterpret_cast<uint32_t*>(ws);
+      a.B = static_cast<int>(nb);
+      a.H = static_cast<int>(nh);
+      a.D = static_cast<int>(p.head_dim);
+      a.n = static_cast<int>(p.seq_k);
+      a.cap = p.seq_k;
+      if (paged) {
+        a.bt = p.block_table + b0 * p.block_table_stride;
+        a.bt_stride = p.block_table_stride;
+        a.page_size = p.page_size;
+        a.num_pages = p.num_pages;
+      }
+      a.vec = true;
+      a.leave_tail = true;  // the prefill never uses what lies past a length
+      int rc = launch_q4_read(a, f16, stream);
+      if (rc != GQA_OK) return rc;
+      rc = launch_prefill_call(
+          c, sms, static_cast<const uint16_t*>(q) + b0 * p.q_stride[0] + h0 * g * p.q_stride[1],
+          ws + s.k_offset, ws + s.v_offset, mask != nullptr ? mask + b0 * p.mask_stride[0] : nullptr,
+          static_cast<uint16_t*>(out) + b0 * p.o_stride[0] + h0 * g * p.o_stride[1], ws, stream);
+      if (rc != GQA_OK) return rc;
+    }
   }
   return GQA_OK;
 }
@@ -134,10 +285,7 @@ int make_rows_args(const gqa_kv_q4_desc* d, void* cache_k, void* cache_v, void* 
   a.B = static_cast<int>(d->batch);
   a.n = static_cast<int>(d->n);
   if (d->batch == 0 || d->n == 0) return GQA_OK;
-  // The kernels count 16-byte pieces of rows in 32 bits.
-  const int64_t per = 8 * q4::groups_of(static_cast<int>(d->head_dim));
-  if (d->batch * d->heads_kv >= kLim / per || d->batch * d->heads_kv * per >= kLim / d->n)
-    return GQA_ERR_UNSUPPORTED;
+  if (d->batch * d->heads_kv >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit head indices
   if (cache_k == nullptr || cache_v == nullptr || k == nullptr || v == nullptr ||
       (append && lens == nullptr))
     return GQA_ERR_NULL;
@@ -244,6 +392,10 @@ GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cac
   if (!aligned(q, 16) || !aligned(cache_k, 16) || !aligned(cache_v, 16) || !aligned(out, 16))
     return GQA_ERR_LAYOUT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (plan.kernel == GQA_KERNEL_Q4_PREFILL)
+    return run_slices(p, plan_slices(p, sms), sms, q, static_cast<const uint8_t*>(cache_k),
+                      static_cast<const uint8_t*>(cache_v), p.has_mask ? mask : nullptr, out, ws,
+                      stream);
   const DecodeShape s = plan_decode_q4(p, sms);
   CUtensorMap tmk, tmv;
   int erc = encode_records(&tmk, cache_k, p, p.k_stride, s.D);

@@ -211,6 +211,11 @@ int launch_prefill(const gqa_problem& p, const PrefillShape& s, const PrefillArg
                    const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                    cudaStream_t stream);
 
+// Both of them: tensor maps, arguments and launches of a validated problem
+// that pick_kernel sends to prefill (api.cu).  `ws` holds plan_prefill's scratch.
+int launch_prefill_call(const gqa_problem& p, int sms, const void* q, const void* k, const void* v,
+                        const uint8_t* mask, void* out, uint8_t* ws, cudaStream_t stream);
+
 // ------------------------------------------------------------ fp32 path
 int launch_f32(const gqa_problem& p, const float* q, const float* k, const float* v,
                const uint8_t* mask, float* out, uint32_t* err, cudaStream_t stream);
@@ -253,6 +258,7 @@ struct Q4RowsArgs {
   const int32_t* bt;        // paged cache: block table, or nullptr
   int64_t bt_stride, page_size, num_pages;
   bool vec;                 // every 16-bit row starts on 16 bytes
+  bool leave_tail;          // read: rows past the length are left as they are, not zeroed
 };
 int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);

@@ -284,18 +284,20 @@ __global__ void __launch_bounds__(kThreads) gqa_q4_read_kernel(const Q4RowsArgs 
     const int64_t start = a.starts != nullptr ? a.starts[b] : a.start;
     if (start < 0) {
       if (first) atomicOr(a.err, kErrKvLength);
-      len = 0;
+      len = start;
     }
     const int64_t* rs = a.rs[kv];
     uint16_t* dst = a.rows[kv] + b * rs[0] + h * rs[1] + d0;
     const int step = per_pass * kRows;
-    for (int t0 = blockIdx.x * step; t0 < a.n; t0 += gridDim.x * step) {
+    const int64_t left = len - start;  // rows that exist
+    const int n = a.leave_tail && left < a.n ? static_cast<int>(left < 0 ? 0 : left) : a.n;
+    for (int t0 = blockIdx.x * step; t0 < n; t0 += gridDim.x * step) {
       uint32_t par[kRows], word[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const int t = t0 + k * per_pass + slot;
         par[k] = word[k] = 0u;  // reads as zeros
-        if (t >= a.n || start + t >= len) continue;
+        if (t >= n || t >= left) continue;
         const int64_t at = record_at(a, kv, b, h, start + t);
         if (at < 0) {
           if (kv == 0 && h == 0 && d0 == 0) atomicOr(a.err, kErrPage);
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) gqa_q4_read_kernel(const Q4RowsArgs 
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const int t = t0 + k * per_pass + slot;
-        if (t >= a.n) continue;
+        if (t >= n) continue;
         const float s = scale_of<F16>(par[k]), m = min_of<F16>(par[k]);
         uint32_t out[4];
 #pragma unroll

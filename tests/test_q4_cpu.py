@@ -164,7 +164,7 @@ def _desc(gqa, B=2, Hkv=2, cap=100, D=64, n=3, **over):
     (dict(v_stride=(384, -192, 64, 1)), 3, 3),
     (dict(block_table=64, block_table_stride=1, page_size=64, num_pages=9), 2, 2),
     (dict(block_table=64, block_table_stride=2, page_size=64, num_pages=0), 2, 2),
-    (dict(batch=1 << 20, heads_kv=1 << 8), 4, 4),  # more pieces than 32 bits count
+    (dict(batch=1 << 20, heads_kv=1 << 12), 4, 4),  # more heads than 32 bits count
     (dict(batch=0), 0, 0),
     (dict(n=0), 0, 0),
 ])

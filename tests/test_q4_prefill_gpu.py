@@ -1,0 +1,161 @@
+"""Long query blocks over the 4-bit cache: records read back into scratch, a
+slice of the heads at a time, and attended to there.  Checked against attention
+in 64 bits (torch, on the device) over the values the records stand for."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import q4_util as u
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gqa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import grouped_query_attention_fwd_b200 as m
+    return m
+
+
+def _records(gqa, B, Hkv, S, D, dtype, seed, keys):
+    """Records written by kv_append_q4 (tested on its own), and their values in
+    float64, decoded from the bytes here."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(B, Hkv, S, D, generator=g, device="cuda")
+    if keys:
+        x += torch.randn(1, Hkv, 1, D, generator=g, device="cuda")
+    x = x.to(u.TORCH[dtype])
+    c = torch.zeros(B, Hkv, S, u.record_bytes(D), dtype=torch.uint8, device="cuda")
+    gqa.kv_append_q4(c, c.clone(), x, x, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    G = -(-D // 32)
+    par = c[..., :4 * G].contiguous().view(u.TORCH[dtype]).double().unflatten(-1, (G, 2))
+    body = c[..., 16:].long()
+    code = torch.stack([body % 16, body // 16], -1).double().flatten(-2).unflatten(-1, (G, 32))
+    return c, (code * par[..., :1] + par[..., 1:]).flatten(-2)[..., :D]
+
+
+CASES = [
+    # B, Hq, Hkv, Sq, Sk, D, dtype, lens, page, window, mask, several slices
+    (4, 8, 2, 512, 2048, 128, "bf16", None, 0, 0, False, False),
+    (4, 8, 2, 512, 2048, 128, "fp16", [2048, 1, 513, 700], 64, 0, False, False),
+    (3, 12, 2, 700, 1536, 64, "bf16", [1536, 900, 701], 128, 300, False, False),
+    (4, 8, 4, 640, 1111, 80, "bf16", None, 0, 0, True, False),
+    (12, 8, 2, 1024, 8192, 128, "bf16", None, 0, 0, False, True),
+    (2, 96, 24, 1024, 8192, 128, "bf16", [8192, 5000], 64, 0, True, True),
+]
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_long_query_blocks(gqa, case):
+    B, Hq, Hkv, Sq, Sk, D, dtype, lens, page, window, masked, several = case
+    ck, k64 = _records(gqa, B, Hkv, Sk, D, dtype, 1, True)
+    cv, v64 = _records(gqa, B, Hkv, Sk, D, dtype, 2, False)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(B, Hq, Sq, D, generator=gen, device="cuda").to(u.TORCH[dtype])
+    kw = dict(causal=True, causal_offset="bottom_right", window=window)
+    held = lens or [Sk] * B
+    if lens:
+        kw["kv_lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        for b in range(B):  # NaN scales past each length
+            ck[b, :, lens[b]:] = cv[b, :, lens[b]:] = 0xFF
+    mask = None
+    if masked:
+        mask = torch.rand(B, Sq, Sk, generator=gen, device="cuda") < 0.7
+        mask[:, 5] = False  # an empty row
+        kw["mask"] = mask
+    if page:
+        rng = np.random.default_rng(0)
+        per = Sk // page
+        order = torch.from_numpy(rng.permutation(B * per + 2)[:B * per].reshape(B, per)).cuda()
+        pools = []
+        for c in (ck, cv):
+            pool = torch.full((B * per + 2, Hkv, page, c.shape[-1]), 0xFF, dtype=torch.uint8,
+                              device="cuda")
+            pool[order] = c.unflatten(2, (per, page)).transpose(1, 2)
+            pools.append(pool)
+        kw["block_table"] = order.int()
+    else:
+        pools = [ck, cv]
+    plan = gqa.query_q4(q, *pools, **kw)
+    assert plan["kernel_name"] == "q4_prefill"
+    per_slice = 2 + (1 if masked else 0) + (1 if masked or lens else 0)
+    assert (plan["launches"] > per_slice) == several
+    # Rows behind the result are left alone: the output is a part of a larger buffer.
+    buf = torch.full((B, Hq, Sq + 1, D), 7.0, dtype=q.dtype, device="cuda")
+    out = gqa.forward_q4(q, *pools, out=buf[:, :, :Sq], **kw)
+    assert gqa.device_status() == gqa.GQA_OK
+    assert torch.all(buf[:, :, Sq] == 7.0)
+
+    g, unit, scale = Hq // Hkv, u.UNIT[dtype], 1.0 / math.sqrt(D)
+    worst, off, norm = 0.0, 0.0, 0.0
+    for b in range(B):
+        n = held[b]
+        i = torch.arange(Sq, device="cuda")[:, None] + n - Sq
+        j = torch.arange(n, device="cuda")[None, :]
+        see = j <= i
+        if window:
+            see &= j > i - window
+        if masked:
+            see &= mask[b, :, :n]
+        for h in range(Hq):
+            k, v = k64[b, h // g, :n], v64[b, h // g, :n]
+            qh = q[b, h].double()
+            s = (qh @ k.T * scale).masked_fill(~see, -math.inf)
+            p = torch.softmax(s, -1)
+            ref = p @ v
+            # Roundings, each at most `unit` relative: keys (a score moves by
+            # at most scale * unit * sum |q k|, a weight by twice that), values,
+            # weights, the output; 2^-14 for fp32 sums and exponentials.
+            move = 2.1 * scale * unit * (qh.abs() @ k.abs().T).amax(-1, keepdim=True)
+            bound = (p @ v.abs()) * (2.02 * unit + move + 2.0 ** -14) + 1.01 * unit * ref.abs() + \
+                2.0 ** -24
+            got = out[b, h].double()
+            empty = ~see.any(-1)
+            assert torch.equal(torch.isnan(got).all(-1), empty)
+            assert torch.equal(torch.isnan(got), torch.isnan(ref))
+            err = (got - ref)[~empty].abs()
+            worst = max(worst, float((err / bound[~empty]).max()) if err.numel() else 0.0)
+            off += float(err.square().sum())
+            norm += float(ref[~empty].square().sum())
+    assert worst <= 1.0, worst
+    assert math.sqrt(off) <= 1e-2 * math.sqrt(norm)
+
+
+def test_chunk_equals_short_blocks(gqa):
+    """The two ways of attending agree: a long block's last rows against a
+    short block of the same queries."""
+    ck, _ = _records(gqa, 4, 2, 2048, 128, "bf16", 5, True)
+    cv, _ = _records(gqa, 4, 2, 2048, 128, "bf16", 6, False)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    q = torch.randn(4, 8, 512, 128, generator=gen, device="cuda").bfloat16()
+    kw = dict(causal=True, causal_offset="bottom_right")
+    assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == "q4_prefill"
+    tail = q[:, :, -4:]
+    assert gqa.query_q4(tail, ck, cv, **kw)["kernel_name"] == "q4"
+    a = gqa.forward_q4(q, ck, cv, **kw)[:, :, -4:].double()
+    b = gqa.forward_q4(tail, ck, cv, **kw).double()
+    assert gqa.device_status() == gqa.GQA_OK
+    assert float((a - b).norm() / b.norm()) <= 1e-2
+
+
+def test_long_block_in_a_graph(gqa):
+    ck, _ = _records(gqa, 4, 2, 2048, 64, "fp16", 8, True)
+    cv, _ = _records(gqa, 4, 2, 2048, 64, "fp16", 9, False)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    q = torch.randn(4, 8, 700, 64, generator=gen, device="cuda").half()
+    lens = torch.tensor([2048, 700, 1500, 2000], dtype=torch.int32, device="cuda")
+    kw = dict(causal=True, causal_offset="bottom_right", kv_lens=lens)
+    assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == "q4_prefill"
+    want = gqa.forward_q4(q, ck, cv, **kw)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = gqa.forward_q4(q, ck, cv, **kw)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
