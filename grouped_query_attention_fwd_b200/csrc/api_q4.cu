@@ -14,10 +14,9 @@ namespace {
 constexpr int64_t kLim = int64_t(1) << 31;
 
 // Times that the choice between the two ways of attending goes by (ns, this
-// library's kernels): launch and ends of a decode, a 128-key unit of one SM at
-// up to 8 and up to 16 rows; a slice's launches and ends, a key tile of the
-// two-tile prefill; bytes read and written by the read back.
-constexpr double kDecodeNs = 10000, kUnitNs = 600, kUnit2Ns = 1200;
+// library's kernels): launch and ends of a decode; a slice's launches and ends,
+// a key tile of the two-tile prefill; bytes read and written by the read back.
+constexpr double kDecodeNs = 10000;
 constexpr double kSliceNs = 12000, kTwoTileNs = 2200, kReadBytesPerNs = 4500;
 
 bool aligned(const void* ptr, uintptr_t a) {
@@ -121,11 +120,11 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
 
 // Estimated time of the decode kernel over the same problem.
 double decode_ns(const DecodeShape& s, int sms) {
-  return kDecodeNs + double(s.units) / sms * (s.NT == 1 ? kUnitNs : kUnit2Ns);
+  return kDecodeNs + double(s.units) / sms * kQ4UnitNs;
 }
 
-// Query blocks of up to 16 rows per kv head take one pass over the records;
-// longer ones take a pass per 16 rows, or go over 16-bit scratch.
+// Query blocks of up to 8 rows per kv head take one pass over the records;
+// longer ones take a pass per 8 rows, or go over 16-bit scratch.
 bool use_slices(const gqa_problem& p, const DecodeShape& d, const SlicePlan& s, int sms) {
   return d.passes > 1 && p.seq_q > 1 && s.ns < decode_ns(d, sms);
 }
@@ -165,10 +164,10 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
   if (s.units >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit unit indices
   plan->kernel = GQA_KERNEL_Q4;
   plan->grid = s.grid;
-  plan->block = decode_q4_threads(s);
+  plan->block = kQ4Threads;
   plan->smem_bytes = s.smem_bytes;
   plan->launches = s.zero_counters ? 2 : 1;
-  plan->work_units = static_cast<int32_t>(s.units);
+  plan->work_units = static_cast<int32_t>(s.groups * s.tiles_per_group);
   plan->workspace_bytes = (s.workspace_end + 255) / 256 * 256;
   return GQA_OK;
 }

@@ -27,10 +27,11 @@
 //  * The weights p_j s_jg are rounded to fp16 (2^-11) as the B operand of
 //    P V in both cache types.  To keep them in fp16's range whatever the
 //    scales, the exponent reference is the running maximum of t_j + log2 of
-//    key j's largest V scale: the weights stay at or below 2^8.  An fp16 cache
-//    also counts its V codes from 8 (one packed subtraction per register), so
-//    that the rounding multiplies at most half of the group's range; bf16
-//    outputs are rounded 8 times more coarsely than the weights as it is.
+//    key j's largest V scale: the weights stay at or below 2^8.  With an
+//    fp16 cache the rounded weights are also summed (a row of ones in an MMA
+//    of its own) and eight of them taken off, so that the rounding multiplies
+//    codes counted from the middle of the group's range, at most half of it;
+//    bf16 outputs are rounded 8 times more coarsely than the weights as it is.
 //  * The reference is lazy: it moves, and the sums are rescaled, only when a
 //    score passes it by more than 2^8, which one vote per chunk finds out.
 //
@@ -55,19 +56,23 @@ namespace {
 using namespace q4;
 
 constexpr int KT = kDecodeKeysPerTile;
-constexpr int kSub = 2;                    // 16-key MMA tiles a warp takes at a time
-constexpr int kChunk = 16 * kSub;          // its keys
-constexpr int kChunks = KT / kChunk;
 constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
 constexpr int kFastMerge = 4;              // contributors of a split group merged directly
 constexpr int kBatch = 8;                  // partials loaded at a time by the other merge
 
-template <int NG, int NT>
+template <int NG>
 struct Q4Layout {
   static constexpr int D = NG * kGroup;            // head_dim, padded
-  static constexpr int HP = 8 * NT;                // rows per pass
-  static constexpr int W = NT == 1 ? 11 : 7;       // consumer warps: 3 (2) per scheduler with the producer
+  static constexpr int HP = 8;                     // rows per pass: the columns of one MMA
+  static constexpr int W = 7;                      // consumer warps: with the producer two per scheduler
+  // 16-key MMA tiles a warp takes at a time: more of them share the waits,
+  // votes and address arithmetic of a chunk (16, 32 and 64 keys took 754, 610
+  // and 560 ns per unit of an SM).
+  static constexpr int kSub = 4;
+  static constexpr int kChunk = 16 * kSub;         // keys of a chunk
+  static constexpr int kChunks = KT / kChunk;
   static constexpr int kThreads = (W + 1) * 32;
+  static_assert(kThreads == kQ4Threads, "the plan reports it");
   static constexpr int kPitch = record_bytes(D);   // bytes per record in shared memory
   static constexpr int kTile = KT * kPitch;        // K (or V) records of a unit
   static constexpr int kStage = 2 * kTile;
@@ -79,6 +84,11 @@ struct Q4Layout {
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
 };
+
+// The lowest n bits (n below 0: none, above 31: all).
+__device__ __forceinline__ uint32_t below(int n) {
+  return n >= 32 ? ~0u : (n <= 0 ? 0u : (1u << n) - 1u);
+}
 
 // D = A B, no accumulator.
 template <bool F16>
@@ -104,29 +114,10 @@ __device__ __forceinline__ void ldmatrix_x2(uint32_t& r0, uint32_t& r1, uint32_t
                : "r"(addr));
 }
 
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 __device__ __forceinline__ float fast_lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// V codes of two keys as an A register: bits 0-3 (or 4-7, times 16) of each
-// half; for an fp16 cache counted from 8 (-8 and -128 smallest fp16 steps).
-template <bool F16>
-__device__ __forceinline__ uint32_t v_codes_lo(uint32_t x) {
-  const uint32_t c = x & 0x000F000Fu;
-  return F16 ? hadd2(c, 0x80088008u) : c;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t v_codes_hi(uint32_t x) {
-  const uint32_t c = x & 0x00F000F0u;
-  return F16 ? hadd2(c, 0x80808080u) : c;
 }
 
 // Record heads: NG words (scale | minimum << 16).
@@ -141,14 +132,17 @@ __device__ __forceinline__ void load_params(uint32_t (&w)[NG], uint32_t addr) {
 }
 
 // MQ: several query positions per kv head; row r = head * seq_q + query.
-template <int NG, int NT, bool MQ, bool F16>
-__global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
+template <int NG, bool MQ, bool F16>
+__global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
     gqa_decode_q4_kernel(const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const DecodeArgs a,
                          const int tiles_per_group, const int passes, const int units,
-                         const int stages, uint32_t* __restrict__ counters) {
-  using L = Q4Layout<NG, NT>;
+                         const int stages, const int split, const int lead,
+                         uint32_t* __restrict__ counters) {
+  using L = Q4Layout<NG>;
   constexpr int HP = L::HP, D = L::D, W = L::W, P = L::kPitch, R = L::kRow;
+  constexpr int kSub = L::kSub, kChunk = L::kChunk, kChunks = L::kChunks;
+  constexpr int NW = kSub / 2;  // 32-key words of a chunk's visibility
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
@@ -199,7 +193,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   Sched sc;
   sc.pre = ragged ? pre_s : nullptr;
   sc.len = ragged ? len_s : nullptr;
-  sc.per_b = gpb * tiles_per_group;
+  sc.per_b = gpb * (tiles_per_group + lead);
   sc.gpb = gpb;
   sc.B = a.B;
   // Nothing global that earlier work on the stream writes is read, and nothing
@@ -218,14 +212,15 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     }
     __syncthreads();
     if (warp == 0) {
-      // pre[b + 1] = sum over entries <= b of (groups per entry) x (tiles of the entry).
+      // pre[b + 1] = sum over entries <= b of (groups per entry) x (places of a group).
       int carry = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
         int v = 0;
         if (b < a.B)
-          v = gpb * decode_key_range(len_s[b], a.Sk, a.Sq, a.causal, a.causal_offset, a.window)
-                        .tiles;
+          v = gpb * (lead + decode_key_range(len_s[b], a.Sk, a.Sq, a.causal, a.causal_offset,
+                                             a.window)
+                                .tiles);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int n = __shfl_up_sync(0xffffffffu, v, o);
@@ -245,36 +240,68 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
   }
   sc.total = ragged ? pre_s[a.B] : units;
   sc.P = static_cast<int>(gridDim.x) < sc.total ? static_cast<int>(gridDim.x) : sc.total;
-  const bool has_range = static_cast<int>(blockIdx.x) < sc.P;
-  const int u_begin = has_range ? range_start(blockIdx.x, sc.total, sc.P) : 0;
-  const int u_end = has_range ? range_start(blockIdx.x + 1, sc.total, sc.P) : 0;
 
+  // The places of a launch: every group has `lead` empty ones (what a change
+  // of groups costs, in units) and then one per unit.  They are cut into one
+  // range per CTA, all equal; or, with `split`, every group into `split` equal
+  // ranges and none shared by two groups (no lead then).
+  auto start_of = [&](int cta) {
+    if (split > 0)
+      return cta / split * tiles_per_group + cta % split * tiles_per_group / split;
+    return range_start(cta, sc.total, sc.P);
+  };
+  auto cta_of = [&](int place) {
+    if (split > 0) {
+      const int g = place / tiles_per_group, r = place - g * tiles_per_group;
+      return g * split + ((r + 1) * split + tiles_per_group - 1) / tiles_per_group - 1;
+    }
+    return cta_of_unit(place, sc.total, sc.P);
+  };
   Cursor cu;
+  auto seek_entry = [&](int place) {  // the cursor at the entry of a place
+    if (cu.b >= 0 && place >= cu.beg && place < cu.end) return;
+    cu.b = sc.batch_of(place);
+    cu.beg = sc.start_of(cu.b);
+    cu.kr = decode_key_range(sc.len ? sc.len[cu.b] : a.Sk, a.Sk, a.Sq, a.causal, a.causal_offset,
+                             a.window);
+    cu.end = cu.beg + gpb * (cu.kr.tiles + lead);
+  };
   // Address of row hl (a head, or a (head, query) pair) of kv head kv of entry b.
   auto q_row = [&](int b, int kv, int hl) {
     const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
     return a.q + b * a.qs[0] + static_cast<int64_t>(kv * a.g + hh) * a.qs[1] +
            static_cast<int64_t>(qi) * a.qs[2];
   };
-  // Group of a unit: its place in the launch, and who shares it.
+  // Group (kv head and pass of one entry) of a place: its index in the launch,
+  // the place of its first unit, its units, and the CTAs that share those.
   struct Group {
     int b, kv, pass, id, beg, tiles, c_lo, c_hi, rows;
   };
-  auto group_at = [&](int u) {
-    seek(cu, u, sc, a);
-    const int gi = (u - cu.beg) / cu.kr.tiles;
+  auto id_at = [&](int place) {
+    seek_entry(place);
+    return cu.b * gpb + (place - cu.beg) / (cu.kr.tiles + lead);
+  };
+  auto group_at = [&](int place) {
     Group g;
+    g.id = id_at(place);
     g.b = cu.b;
+    const int gi = g.id - cu.b * gpb;
     g.kv = gi / passes;
-    g.pass = gi % passes;
-    g.id = cu.b * gpb + gi;
-    g.beg = cu.beg + gi * cu.kr.tiles;
+    g.pass = gi - g.kv * passes;
+    g.beg = cu.beg + gi * (cu.kr.tiles + lead) + lead;
     g.tiles = cu.kr.tiles;
-    g.c_lo = cta_of_unit(g.beg, sc.total, sc.P);
-    g.c_hi = cta_of_unit(g.beg + g.tiles - 1, sc.total, sc.P);
+    g.c_lo = cta_of(g.beg);
+    g.c_hi = cta_of(g.beg + g.tiles - 1);
     g.rows = min(HP, a.rows - g.pass * HP);
     return g;
   };
+  const bool has_range = static_cast<int>(blockIdx.x) < sc.P;
+  const int v_begin = has_range ? start_of(blockIdx.x) : 0;
+  int v_end = has_range ? start_of(blockIdx.x + 1) : 0;
+  if (v_begin < v_end) {  // a range that ends in a group's lead has no unit of that group
+    const Group g = group_at(v_end - 1);
+    if (v_end <= g.beg) v_end = max(v_begin, g.beg - lead);
+  }
 
   if (warp == W) {
     // ------------------------------------------------------------ producer
@@ -293,22 +320,23 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       prefetch_tmap(&tmk);
       prefetch_tmap(&tmv);
     }
-    for (int ua = u_begin; ua < u_end && ok;) {
-      const Group grp = group_at(ua);
-      const int ub = min(u_end, grp.beg + grp.tiles);
+    for (int va = v_begin; va < v_end && ok;) {
+      const Group grp = group_at(va);
+      const int t0 = max(va - grp.beg, 0);               // units [t0, t1) of the group
+      const int t1 = min(v_end - grp.beg, grp.tiles);
       const int kv = grp.kv, b = grp.b;
-      int key0 = (ua - grp.beg + cu.kr.t0) * KT;
-      if (ua == u_begin && !ragged) {
+      int key0 = (t0 + cu.kr.t0) * KT;
+      if (va == v_begin && !ragged) {
         // Contiguous caches: the first units start towards L2 before the grid
         // dependency resolves (earlier work may still be writing the cache;
         // these are hints, the copies below read what it wrote).
-        if (!paged && lane < 2 && ua + lane < ub) {
+        if (!paged && lane < 2 && t0 + lane < t1) {
           tma_prefetch_4d(&tmk, 0, key0 + lane * KT, kv, b);
           tma_prefetch_4d(&tmv, 0, key0 + lane * KT, kv, b);
         }
         griddep_wait();
       }
-      if (a.trace != nullptr && lane == 0 && ua == u_begin) trace()[kTrReady] = globaltimer_ns();
+      if (a.trace != nullptr && lane == 0 && va == v_begin) trace()[kTrReady] = globaltimer_ns();
       const int len = sc.len ? sc.len[b] : a.Sk;
       // Page and row of a 64-key box; one past the sequence's length takes
       // page num_pages, which is out of range: TMA fills it with zeros.
@@ -320,12 +348,12 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         return a.num_pages;  // read as zeros
       };
       const int at = (lane >> 1) * KT + (lane & 1) * kDecodePageBox;
-      int next_page = paged ? page_of(key0 + at, ua + (lane >> 1) < ub) : 0;
-      for (int u = ua; u < ub && ok;) {
+      int next_page = paged ? page_of(key0 + at, t0 + (lane >> 1) < t1) : 0;
+      for (int u = t0; u < t1 && ok;) {
         const int my_page = next_page;
         const int my_row = paged ? (key0 + at) % a.page_size : 0;
-        const int u_stop = min(u + kBlock, ub);
-        if (paged) next_page = page_of(key0 + kBlock * KT + at, u + kBlock + (lane >> 1) < ub);
+        const int u_stop = min(u + kBlock, t1);
+        if (paged) next_page = page_of(key0 + kBlock * KT + at, u + kBlock + (lane >> 1) < t1);
         for (int i = 0; u < u_stop; ++u, ++i, key0 += KT) {
           int page[2] = {0, 0}, row[2] = {0, 0};
           if (paged) {
@@ -339,7 +367,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_try_wait(&empty[s], parity) ||
                                            mbar_wait(&empty[s], parity, abort_flag, a.err,
                                                      kErrDecodeWait, a.wait_ns));
-          if (ok && u == a.withhold_unit) {
+          if (ok && grp.beg - lead * (grp.id + 1) + u == a.withhold_unit) {
             // Test of the bounded waits, as in the 16-bit decode: nothing more
             // is issued, and the consumers' wait for this unit runs out.
             const uint64_t t0 = globaltimer_ns();
@@ -373,12 +401,13 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           }
         }
       }
-      if (ua == u_begin && ub < u_end && ok) {
+      const int vb = grp.beg + t1;
+      if (va == v_begin && vb < v_end && ok) {
         // The Q rows of the range's second group: at the change of groups
         // they would cost the consumers a round trip.  (The first group's
         // come while its first unit does; a range over more groups has short
         // ones, and the consumers fetch the others' when they get there.)
-        const Group next = group_at(ub);
+        const Group next = group_at(vb);
         if (lane == 0)
           mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(next.rows * a.Dv * 2));
         __syncwarp();
@@ -387,23 +416,20 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
                     static_cast<uint32_t>(a.Dv * 2), q_full);
         q_sent = true;
       }
-      ua = ub;
+      va = vb;
     }
     if (lane == 0) {
       if (a.trace != nullptr) trace()[kTrLastIssue] = globaltimer_ns();
       // Final group split over several CTAs: once the consumers are on the
       // range's last unit, read its ticket count for their final merge (the
       // fence makes the partials published before those tickets visible).
-      if (!*abort_flag && u_begin < u_end) {
-        seek(cu, u_end - 1, sc, a);
-        const int gi = (u_end - 1 - cu.beg) / cu.kr.tiles;
-        const int g_beg = cu.beg + gi * cu.kr.tiles;
-        if (cta_of_unit(g_beg, sc.total, sc.P) !=
-            cta_of_unit(g_beg + cu.kr.tiles - 1, sc.total, sc.P)) {
+      if (!*abort_flag && v_begin < v_end) {
+        const Group g = group_at(v_end - 1);
+        if (g.c_lo != g.c_hi) {
           const int j = it - 2;  // second-to-last unit of the range
           if (j < 0 || mbar_wait(&empty[j % stages], static_cast<uint32_t>((j / stages) & 1),
                                  abort_flag, a.err, kErrDecodeWait, a.wait_ns)) {
-            const uint32_t n = ld_relaxed_gpu(&counters[cu.b * gpb + gi]);
+            const uint32_t n = ld_relaxed_gpu(&counters[g.id]);
             fence_acq_rel_gpu();
             *peek_count = n;
           }
@@ -436,8 +462,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     // Partial slot of a CTA for a split group: only a range's first and last
     // group can be split, so there are two.
     auto slot_of = [&](int cta, int id) {
-      const int first = group_of(range_start(cta, sc.total, sc.P), sc, a);
-      return (cta * 2 + (first == id ? 0 : 1)) * HP;
+      return (cta * 2 + (id_at(start_of(cta)) == id ? 0 : 1)) * HP;
     };
     // All partials of a split group are published: their merge by the whole
     // consumer group, eight contributors' loads in flight at a time.
@@ -490,35 +515,36 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
     };
 
     int n_flush = 0;           // groups whose states went through the scratch
-    int u_second = u_end;      // first unit of the range's second group
-    for (int ua = u_begin; ua < u_end;) {
-      // One group (kv head and pass of one entry): units [ua, ub) of this range.
-      const Group grp = group_at(ua);
-      const int ub = min(u_end, grp.beg + grp.tiles);
-      const int tile0 = ua - grp.beg + cu.kr.t0;
+    int v_second = v_end;      // where the range's second group begins
+    int done = 0;              // units of the groups before
+    for (int va = v_begin; va < v_end;) {
+      // One group (kv head and pass of one entry): units [t0, t1) of it.
+      const Group grp = group_at(va);
+      const int t0 = max(va - grp.beg, 0);
+      const int t1 = min(v_end - grp.beg, grp.tiles);
+      const int vb = grp.beg + t1;
       const int kv = grp.kv, pass = grp.pass, b = grp.b;
       const int len = sc.len ? sc.len[b] : a.Sk;
-      if (ua == u_begin) {
-        u_second = ub;
+      const KeyRange kr = cu.kr;
+      if (va == v_begin) {
+        v_second = vb;
         if (!ragged) griddep_wait();
       }
       // (A wait that gave up sets the abort flag: the arithmetic goes on with
       // whatever is there, the result is undefined.)
-      const bool stashed = ua == u_second;
+      const bool stashed = va == v_second;
       if (stashed) mbar_wait(q_full, 0, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
 
-      // Q as B fragments, thread (r8, c): row r8 of each column tile, dims
-      // 32 t + 8 c .. + 7; and the sums over each group's dims, the factors
-      // of the minima, as two 16-bit parts: a record's head is the A operand
-      // of a product of its own, and its scales meet zeros.
-      uint32_t bq[NT][NG][4], bm[NT][2];
-      float fac[NT][2];
-      int vlo[NT][2], vhi[NT][2];          // visible keys of this thread's two rows (MQ)
-      const uint8_t* vmask[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int hl = pass * HP + nt * 8 + r8;
-        const uint16_t* qrow = stashed ? q_next + (nt * 8 + r8) * D : q_row(b, kv, hl);
+      // Q as B fragments, thread (r8, c): row r8 of the pass, dims 32 t + 8 c
+      // .. + 7; and the sums over each group's dims, the factors of the
+      // minima, as two 16-bit parts: a record's head is the A operand of a
+      // product of its own, and its scales meet zeros.
+      uint32_t bq[NG][4], bm[2];
+      float fac[2];         // what turns this thread's two rows' scores into base 2
+      int vlo[2], vhi[2];   // their visible keys, without the mask
+      {
+        const int hl = pass * HP + r8;
+        const uint16_t* qrow = stashed ? q_next + r8 * D : q_row(b, kv, hl);
         float f[NG][8];
         float amax = 0.f;
 #pragma unroll
@@ -558,39 +584,36 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           s += __shfl_xor_sync(0xffffffffu, s, 2);
           if (t == c) mine = s / back;  // a power of two: exact
           const float odd = up * 0.0625f;
-          bq[nt][t][0] = pack2<F16>(f[t][0] * up, f[t][4] * up);
-          bq[nt][t][1] = pack2<F16>(f[t][1] * odd, f[t][5] * odd);
-          bq[nt][t][2] = pack2<F16>(f[t][2] * up, f[t][6] * up);
-          bq[nt][t][3] = pack2<F16>(f[t][3] * odd, f[t][7] * odd);
+          bq[t][0] = pack2<F16>(f[t][0] * up, f[t][4] * up);
+          bq[t][1] = pack2<F16>(f[t][1] * odd, f[t][5] * odd);
+          bq[t][2] = pack2<F16>(f[t][2] * up, f[t][6] * up);
+          bq[t][3] = pack2<F16>(f[t][3] * odd, f[t][7] * odd);
         }
         const uint32_t high = to_16<F16>(mine);
-        bm[nt][0] = high << 16;
-        bm[nt][1] = to_16<F16>(mine - to_f32<F16>(high)) << 16;
+        bm[0] = high << 16;
+        bm[1] = to_16<F16>(mine - to_f32<F16>(high)) << 16;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int src = (2 * c + e) * 4;
-          fac[nt][e] = a.scale_log2 * __shfl_sync(0xffffffffu, back, src);
-          const int row = pass * HP + nt * 8 + 2 * c + e;
-          const int i = MQ ? (row < a.rows ? row : 0) % a.Sq : 0;
-          vlo[nt][e] = cu.kr.lo;
-          vhi[nt][e] = cu.kr.hi;
+          fac[e] = a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * c + e) * 4);
+          vlo[e] = kr.lo;
+          vhi[e] = kr.hi;
           if (MQ) {
+            const int row = pass * HP + 2 * c + e;
+            const int i = (row < a.rows ? row : 0) % a.Sq;
             const int64_t top = i + a.causal_offset + (len - a.Sk);  // query i's diagonal
             int64_t lo = 0, hi = len;
             if (a.causal) {
               hi = top + 1 < hi ? top + 1 : hi;
               if (a.window > 0 && top - a.window + 1 > 0) lo = top - a.window + 1;
             }
-            vlo[nt][e] = static_cast<int>(lo < len ? lo : len);
-            vhi[nt][e] = static_cast<int>(hi > 0 ? hi : 0);
+            vlo[e] = static_cast<int>(lo < len ? lo : len);
+            vhi[e] = static_cast<int>(hi > 0 ? hi : 0);
           }
-          vmask[nt][e] =
-              a.mask ? a.mask + b * a.ms[0] + static_cast<int64_t>(i) * a.ms[1] : nullptr;
         }
       }
-      // Keys that every row sees (without a mask): the first query's upper
-      // limit, the last query's lower one.
-      int all_lo = cu.kr.lo, all_hi = cu.kr.hi;
+      // Keys that every query sees (without a mask): the first one's upper
+      // limit, the last one's lower limit.
+      int all_lo = kr.lo, all_hi = kr.hi;
       if (MQ && a.causal) {
         const int64_t top0 = a.causal_offset + (len - a.Sk);
         all_hi = static_cast<int>(top0 + 1 < 0 ? 0 : (top0 + 1 < len ? top0 + 1 : len));
@@ -599,28 +622,34 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           all_lo = static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
         }
       }
+      // With a mask: the pass's queries, in row order from qi0 (wrapping), and
+      // which of them this thread's rows are.
+      const int nq = MQ ? min(a.Sq, HP) : 1;
+      const int qi0 = MQ ? pass * HP % a.Sq : 0;
+      auto query_of = [&](int e) { return !MQ ? 0 : (a.Sq < HP ? (2 * c + e) % a.Sq : 2 * c + e); };
 
-      float o[NT][NG][2][4], corr[NT][NG][2];
+      float o[NG][2][4], corr[NG][2];
+      float osum[4];  // fp16: lanes 4 t + c hold group t's summed weights
       // The exponent reference (running maximum), its negative with 0 for
-      // -inf, and the score above which it moves.
-      float m_ref[NT][2], m_neg[NT][2], m_top[NT][2], l[NT][2];
+      // -inf, the score above which it moves, and the sum of the weights.
+      float m_ref[2], m_neg[2], m_top[2], l[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int x = 0; x < 4; ++x) osum[x] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          m_ref[nt][e] = m_top[nt][e] = -INFINITY;
-          m_neg[nt][e] = l[nt][e] = 0.f;
+      for (int e = 0; e < 2; ++e) {
+        m_ref[e] = m_top[e] = -INFINITY;
+        m_neg[e] = l[e] = 0.f;
 #pragma unroll
-          for (int t = 0; t < NG; ++t) {
-            corr[nt][t][e] = 0.f;
+        for (int t = 0; t < NG; ++t) {
+          corr[t][e] = 0.f;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) o[nt][t][e][x] = 0.f;
-          }
+          for (int x = 0; x < 4; ++x) o[t][e][x] = 0.f;
         }
+      }
 
       // Chunks of the CTA's range are numbered through; warp w takes those
       // that are w modulo W.
-      const int x0 = (ua - u_begin) * kChunks, x1 = (ub - u_begin) * kChunks;
+      const int x0 = done * kChunks, x1 = (done + t1 - t0) * kChunks;
       int x = x0 + (warp - x0 % W + W) % W;
       int s = (x / kChunks) % stages;
       uint32_t parity = static_cast<uint32_t>((x / kChunks) / stages) & 1u;
@@ -631,14 +660,59 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
             parity ^= 1u;
           }
         const int chunk = x % kChunks;
-        const int key0 = (tile0 + it - (ua - u_begin)) * KT + chunk * kChunk;
+        const int key0 = (t0 + kr.t0 + it - done) * KT + chunk * kChunk;
+        // Visible keys of the chunk, one bit each, where some are not: the
+        // range of each row, and the mask's bytes of each query, a key per
+        // lane, gathered by a ballot.
+        uint32_t vis[2][NW];
+        bool whole = key0 >= all_lo && key0 + kChunk <= all_hi;
+        bool none = key0 >= kr.hi || key0 + kChunk <= kr.lo;
+        if (!none && (!whole || a.has_mask)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+              vis[e][w] = below(vhi[e] - key0 - 32 * w) & ~below(vlo[e] - key0 - 32 * w);
+          if (a.has_mask) {
+            uint32_t on[2][NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) on[0][w] = on[1][w] = 0u;
+#pragma unroll 4
+            for (int i = 0; i < nq; ++i) {
+              const int qi = qi0 + i < a.Sq ? qi0 + i : qi0 + i - a.Sq;
+              const uint8_t* row = a.mask + b * a.ms[0] + static_cast<int64_t>(qi) * a.ms[1];
+#pragma unroll
+              for (int w = 0; w < NW; ++w) {
+                const int key = key0 + 32 * w + lane;
+                const uint32_t bits = __ballot_sync(0xffffffffu, key < kr.hi && row[key] != 0);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (!MQ || query_of(e) == i) on[e][w] = bits;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int w = 0; w < NW; ++w) vis[e][w] &= on[e][w];
+          }
+          uint32_t all = ~0u, any = 0u;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+              all &= vis[e][w];
+              any |= vis[e][w];
+            }
+          whole = __all_sync(0xffffffffu, all == ~0u);
+          none = !__any_sync(0xffffffffu, any != 0u);
+        }
         const bool landed =
             mbar_try_wait(&full[s], parity) ||
             mbar_wait(&full[s], parity, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
         if (a.trace != nullptr && x == 0 && lane == 0) trace()[kTrFirstLand] = globaltimer_ns();
         // (A wait that gave up sets the abort flag: the arithmetic is skipped,
         // the walk goes on, so that all warps reach the same barriers.)
-        if (!__all_sync(0xffffffffu, landed) || key0 >= cu.kr.hi || key0 + kChunk <= cu.kr.lo) {
+        if (!__all_sync(0xffffffffu, landed) || none) {
           if (lane == 0) mbar_arrive(&empty[s]);
           continue;
         }
@@ -648,7 +722,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         const uint32_t at =
             (((lane >> 3) & 1) * 8 + (lane & 7)) * P + kHeadBytes + (lane >> 4) * 16;
 
-        float sv[kSub][NT][4];  // scores: keys r8 (0, 1) and r8 + 8 (2, 3), rows 2 c + {0, 1}
+        float sv[kSub][4];  // scores: keys r8 (0, 1) and r8 + 8 (2, 3), rows 2 c + {0, 1}
 #pragma unroll
         for (int j = 0; j < kSub; ++j) {
           const uint32_t kj = kb + j * 16 * P;
@@ -659,24 +733,18 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
           ldmatrix_x2(h0, h1, kj + (lane & 15) * P);
           load_params<NG>(kp[0], kj + r8 * P);
           load_params<NG>(kp[1], kj + (r8 + 8) * P);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma_zero<F16>(sv[j][nt], h0, h1, h0, h1, bm[nt][0], bm[nt][1]);
+          mma_zero<F16>(sv[j], h0, h1, h0, h1, bm[0], bm[1]);
 #pragma unroll
           for (int t = 0; t < NG; ++t) {
             const uint32_t a8 = kw[t][0] >> 8, b8 = kw[t][1] >> 8;
+            float acc[4];
+            mma_zero<F16>(acc, kw[t][0] & 0x000F000Fu, kw[t][1] & 0x000F000Fu,
+                          kw[t][0] & 0x00F000F0u, kw[t][1] & 0x00F000F0u, bq[t][0], bq[t][1]);
+            mma_16816<F16>(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
+                           b8 & 0x00F000F0u, bq[t][2], bq[t][3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float acc[4];
-              mma_zero<F16>(acc, kw[t][0] & 0x000F000Fu, kw[t][1] & 0x000F000Fu,
-                            kw[t][0] & 0x00F000F0u, kw[t][1] & 0x00F000F0u, bq[nt][t][0],
-                            bq[nt][t][1]);
-              mma_16816<F16>(acc, a8 & 0x000F000Fu, b8 & 0x000F000Fu, a8 & 0x00F000F0u,
-                             b8 & 0x00F000F0u, bq[nt][t][2], bq[nt][t][3]);
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                sv[j][nt][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y], sv[j][nt][y]);
-            }
+            for (int y = 0; y < 4; ++y)
+              sv[j][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y], sv[j][y]);
           }
         }
         // log2 of each key's largest V scale (see the top), within 2^-60 .. 2^100.
@@ -694,55 +762,51 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
             lsv[j][k] = fast_lg2(fminf(m, 0x1p100f));
           }
 
-        auto rest = [&](auto whole) {
-          constexpr bool kWhole = decltype(whole)::value;
+        auto rest = [&](auto all_seen) {
+          constexpr bool kWhole = decltype(all_seen)::value;
           // Scores in base 2 are sv * fac; with hidden keys the product is
           // taken first and replaced by -inf.
           bool raise = false;
-          bool seen[kSub][NT][4];
+          bool seen[kSub][4];
 #pragma unroll
           for (int j = 0; j < kSub; ++j)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int e = y & 1, key = key0 + j * 16 + r8 + (y >> 1) * 8;
-                float& t = sv[j][nt][y];
-                seen[j][nt][y] = kWhole || (key >= vlo[nt][e] && key < vhi[nt][e] &&
-                                            mask_allows(vmask[nt][e], key));
-                if (!kWhole) t = seen[j][nt][y] ? t * fac[nt][e] : -INFINITY;
-                raise |= fmaf(t, kWhole ? fac[nt][e] : 1.f, lsv[j][y >> 1]) > m_top[nt][e];
-              }
+            for (int y = 0; y < 4; ++y) {
+              const int e = y & 1;
+              float& t = sv[j][y];
+              seen[j][y] =
+                  kWhole || ((vis[e][j >> 1] >> (r8 + 16 * (j & 1) + 8 * (y >> 1))) & 1u) != 0u;
+              if (!kWhole) t = seen[j][y] ? t * fac[e] : -INFINITY;
+              raise |= fmaf(t, kWhole ? fac[e] : 1.f, lsv[j][y >> 1]) > m_top[e];
+            }
           if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 2; ++e) {
+              const float f = kWhole ? fac[e] : 1.f;
+              float mx = -INFINITY;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float f = kWhole ? fac[nt][e] : 1.f;
-                float mx = -INFINITY;
+              for (int j = 0; j < kSub; ++j)
+                mx = fmax3(mx, fmaf(sv[j][e], f, lsv[j][0]), fmaf(sv[j][2 + e], f, lsv[j][1]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float m_new = fmaxf(m_ref[e], mx);
+              m_neg[e] = -exp_ref(m_new);
+              const float alpha = fast_exp2(m_ref[e] + m_neg[e]);
+              m_ref[e] = m_new;
+              m_top[e] = m_new + kLazyLog2;
+              l[e] *= alpha;
+              if (F16) osum[e] *= alpha;
 #pragma unroll
-                for (int j = 0; j < kSub; ++j)
-                  mx = fmax3(mx, fmaf(sv[j][nt][e], f, lsv[j][0]),
-                             fmaf(sv[j][nt][2 + e], f, lsv[j][1]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                const float m_new = fmaxf(m_ref[nt][e], mx);
-                m_neg[nt][e] = -exp_ref(m_new);
-                const float alpha = fast_exp2(m_ref[nt][e] + m_neg[nt][e]);
-                m_ref[nt][e] = m_new;
-                m_top[nt][e] = m_new + kLazyLog2;
-                l[nt][e] *= alpha;
+              for (int t = 0; t < NG; ++t) {
+                corr[t][e] *= alpha;
 #pragma unroll
-                for (int t = 0; t < NG; ++t) {
-                  corr[nt][t][e] *= alpha;
-#pragma unroll
-                  for (int u = 0; u < 2; ++u) {
-                    o[nt][t][u][e] *= alpha;
-                    o[nt][t][u][2 + e] *= alpha;
-                  }
+                for (int u = 0; u < 2; ++u) {
+                  o[t][u][e] *= alpha;
+                  o[t][u][2 + e] *= alpha;
                 }
               }
+            }
           }
 #pragma unroll
           for (int j = 0; j < kSub; ++j) {
@@ -758,59 +822,53 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
               if (lane == 0) mbar_arrive(&empty[s]);
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int y = 0; y < 4; ++y)
+              sv[j][y] = fast_exp2(fmaf(sv[j][y], kWhole ? fac[y & 1] : 1.f, m_neg[y & 1]));
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                sv[j][nt][y] = fast_exp2(fmaf(sv[j][nt][y], kWhole ? fac[nt][y & 1] : 1.f,
-                                              m_neg[nt][y & 1]));
-#pragma unroll
-              for (int e = 0; e < 2; ++e) l[nt][e] += sv[j][nt][e] + sv[j][nt][2 + e];
-            }
+            for (int e = 0; e < 2; ++e) l[e] += sv[j][e] + sv[j][2 + e];
 #pragma unroll
             for (int t = 0; t < NG; ++t) {
-              const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
-              uint32_t pb[NT][2];
+              uint32_t pb[2];
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float scale = scale_of<F16>(vp[k][t]);
-                  float add = min_of<F16>(vp[k][t]);
-                  if (F16) add = fmaf(8.f, scale, add);
-                  const float p0 = sv[j][nt][2 * k], p1 = sv[j][nt][2 * k + 1];
-                  float w0 = p0 * scale, w1 = p1 * scale;
-                  if (kWhole) {
-                    corr[nt][t][0] = fmaf(p0, add, corr[nt][t][0]);
-                    corr[nt][t][1] = fmaf(p1, add, corr[nt][t][1]);
-                  } else {  // a hidden key's parameters may be NaN
-                    w0 = seen[j][nt][2 * k] ? w0 : 0.f;
-                    w1 = seen[j][nt][2 * k + 1] ? w1 : 0.f;
-                    corr[nt][t][0] += seen[j][nt][2 * k] ? p0 * add : 0.f;
-                    corr[nt][t][1] += seen[j][nt][2 * k + 1] ? p1 * add : 0.f;
-                  }
-                  pb[nt][k] = movmatrix_trans(pack_f16x2(w0, w1));
+              for (int k = 0; k < 2; ++k) {
+                const float scale = scale_of<F16>(vp[k][t]);
+                float add = min_of<F16>(vp[k][t]);
+                if (F16) add = fmaf(8.f, scale, add);
+                const float p0 = sv[j][2 * k], p1 = sv[j][2 * k + 1];
+                float w0 = p0 * scale, w1 = p1 * scale;
+                if (kWhole) {
+                  corr[t][0] = fmaf(p0, add, corr[t][0]);
+                  corr[t][1] = fmaf(p1, add, corr[t][1]);
+                } else {  // a hidden key's parameters may be NaN
+                  w0 = seen[j][2 * k] ? w0 : 0.f;
+                  w1 = seen[j][2 * k + 1] ? w1 : 0.f;
+                  corr[t][0] += seen[j][2 * k] ? p0 * add : 0.f;
+                  corr[t][1] += seen[j][2 * k + 1] ? p1 * add : 0.f;
                 }
-              const uint32_t x0 = v_codes_lo<F16>(vw[t][0]), x1 = v_codes_hi<F16>(vw[t][0]);
-              const uint32_t x2 = v_codes_lo<F16>(vw[t][1]), x3 = v_codes_hi<F16>(vw[t][1]);
-              const uint32_t y0 = v_codes_lo<F16>(v0), y1 = v_codes_hi<F16>(v0);
-              const uint32_t y2 = v_codes_lo<F16>(v1), y3 = v_codes_hi<F16>(v1);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(o[nt][t][0], x0, x1, x2, x3, pb[nt][0], pb[nt][1]);
-                mma_f16_16816(o[nt][t][1], y0, y1, y2, y3, pb[nt][0], pb[nt][1]);
+                pb[k] = movmatrix_trans(pack_f16x2(w0, w1));
+              }
+              const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
+              mma_f16_16816(o[t][0], vw[t][0] & 0x000F000Fu, vw[t][0] & 0x00F000F0u,
+                            vw[t][1] & 0x000F000Fu, vw[t][1] & 0x00F000F0u, pb[0], pb[1]);
+              mma_f16_16816(o[t][1], v0 & 0x000F000Fu, v0 & 0x00F000F0u, v1 & 0x000F000Fu,
+                            v1 & 0x00F000F0u, pb[0], pb[1]);
+              if (F16) {  // ones in row t: the group's sum of weights
+                const uint32_t one = r8 == t ? 0x3C003C00u : 0u;
+                mma_f16_16816(osum, one, 0u, one, 0u, pb[0], pb[1]);
               }
             }
           }
         };
-        if (!a.has_mask && key0 >= all_lo && key0 + kChunk <= all_hi)
+        if (whole)
           rest(BoolConst<true>{});
         else
           rest(BoolConst<false>{});
       }
 
       // ---- end of the group: the W warps' states meet in shared memory.
-      if (a.trace != nullptr && threadIdx.x == 0 && ub == u_end) trace()[kTrLastTile] = globaltimer_ns();
-      const bool final_group = ub == u_end;
+      if (a.trace != nullptr && threadIdx.x == 0 && vb == v_end) trace()[kTrLastTile] = globaltimer_ns();
+      const bool final_group = vb == v_end;
+      done += t1 - t0;
       const int n_contrib = grp.c_hi - grp.c_lo + 1;
       if (final_group && threadIdx.x == 0) {
         // The other contributors of the range's last group have mostly
@@ -832,27 +890,24 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
       ++n_flush;
       float* mine = scr + warp * HP * R;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int e = 0; e < 2; ++e) {
+        float* row = mine + (2 * c + e) * R;
+        float lv = l[e];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = nt * 8 + 2 * c + e;
-          float lv = l[nt][e];
+        for (int i = 4; i < 32; i <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, i);
 #pragma unroll
-          for (int i = 4; i < 32; i <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, i);
+        for (int t = 0; t < NG; ++t) {
+          float cv = corr[t][e];
 #pragma unroll
-          for (int t = 0; t < NG; ++t) {
-            float cv = corr[nt][t][e];
-#pragma unroll
-            for (int i = 4; i < 32; i <<= 1) cv += __shfl_xor_sync(0xffffffffu, cv, i);
-            // Codes carry 2^-24, those of odd nibbles 2^-20.
-            const float4 ov = make_float4(fmaf(o[nt][t][0][e], 0x1p24f, cv),
-                                          fmaf(o[nt][t][0][2 + e], 0x1p20f, cv),
-                                          fmaf(o[nt][t][1][e], 0x1p24f, cv),
-                                          fmaf(o[nt][t][1][2 + e], 0x1p20f, cv));
-            *reinterpret_cast<float4*>(mine + h * R + 32 * t + 4 * r8) = ov;
-          }
-          if (r8 == 0) *reinterpret_cast<float2*>(mine + h * R + D) = make_float2(m_ref[nt][e], lv);
+          for (int i = 4; i < 32; i <<= 1) cv += __shfl_xor_sync(0xffffffffu, cv, i);
+          if (F16) cv -= 8.f * __shfl_sync(0xffffffffu, osum[e], 4 * t + c);
+          // Codes carry 2^-24, those of odd nibbles 2^-20.
+          *reinterpret_cast<float4*>(row + 32 * t + 4 * r8) =
+              make_float4(fmaf(o[t][0][e], 0x1p24f, cv), fmaf(o[t][0][2 + e], 0x1p20f, cv),
+                          fmaf(o[t][1][e], 0x1p24f, cv), fmaf(o[t][1][2 + e], 0x1p20f, cv));
         }
+        if (r8 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m_ref[e], lv);
+      }
       const int quads = grp.rows * (D / 4);
       // Row hr of the pass, dims 4 d4 .. + 3 over the W states: (M, l, O).
       auto merge_warps = [&](int hr, int d4, float& M, float& lsum, float4& acc) {
@@ -918,7 +973,7 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
             if (a.trace != nullptr) trace()[kTrFlushes] += 1;
           }
         }
-        ua = ub;
+        va = vb;
         continue;
       }
       sync_consumers();
@@ -987,28 +1042,28 @@ __global__ void __launch_bounds__(Q4Layout<NG, NT>::kThreads, 1)
         trace()[kTrFinalDone] = globaltimer_ns();
         trace()[kTrFinalKind] = n_contrib == 1 ? 0 : (*fast_flag ? 2 : 1);
       }
-      ua = ub;
+      va = vb;
     }
     // The range's first group, where it ended before the range did and this
     // CTA turned out to be the last of its contributors.  (Its merge, before
     // the final group's, set the flag.)
-    if (u_second < u_end) {
+    if (v_second < v_end) {
       sync_consumers();
-      if (*mid_last) merge_partials(group_at(u_begin));
+      if (*mid_last) merge_partials(group_at(v_begin));
     }
   }
   __syncthreads();
   if (a.trace != nullptr && threadIdx.x == 0) {
     trace()[kTrExit] = globaltimer_ns();
     trace()[kTrSm] = static_cast<uint64_t>(sm_id()) | (static_cast<uint64_t>(blockIdx.x) << 32);
-    trace()[kTrUnits] = static_cast<uint64_t>(u_end - u_begin);
+    trace()[kTrUnits] = static_cast<uint64_t>(v_end - v_begin);
   }
 }
 
-template <int NG, int NT, bool MQ, bool F16>
+template <int NG, bool MQ, bool F16>
 int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
              const CUtensorMap& tmv, cudaStream_t stream) {
-  auto kern = gqa_decode_q4_kernel<NG, NT, MQ, F16>;
+  auto kern = gqa_decode_q4_kernel<NG, MQ, F16>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem_bytes) !=
       cudaSuccess) {
     cudaGetLastError();
@@ -1016,7 +1071,7 @@ int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(s.grid));
-  cfg.blockDim = dim3(Q4Layout<NG, NT>::kThreads);
+  cfg.blockDim = dim3(kQ4Threads);
   cfg.dynamicSmemBytes = static_cast<size_t>(s.smem_bytes);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1025,27 +1080,27 @@ int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a, s.tiles_per_group, s.passes,
-                         static_cast<int>(s.units), s.stages, a.counters) != cudaSuccess) {
+                         static_cast<int>(s.units), s.stages, s.split, s.lead, a.counters) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
   return GQA_OK;
 }
 
-template <int NG, int NT>
-int launch_nt(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
+template <int NG>
+int launch_ng(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
               const CUtensorMap& tmv, cudaStream_t stream, bool f16) {
   if (a.Sq > 1)
-    return f16 ? launch_t<NG, NT, true, true>(s, a, tmk, tmv, stream)
-               : launch_t<NG, NT, true, false>(s, a, tmk, tmv, stream);
-  return f16 ? launch_t<NG, NT, false, true>(s, a, tmk, tmv, stream)
-             : launch_t<NG, NT, false, false>(s, a, tmk, tmv, stream);
+    return f16 ? launch_t<NG, true, true>(s, a, tmk, tmv, stream)
+               : launch_t<NG, true, false>(s, a, tmk, tmv, stream);
+  return f16 ? launch_t<NG, false, true>(s, a, tmk, tmv, stream)
+             : launch_t<NG, false, false>(s, a, tmk, tmv, stream);
 }
 
-template <int NG, int NT>
+template <int NG>
 void fit(DecodeShape& s, int ragged_batch) {
   for (s.stages = 10;; --s.stages) {
-    s.smem_bytes = Q4Layout<NG, NT>::bytes(s.stages, ragged_batch);
+    s.smem_bytes = Q4Layout<NG>::bytes(s.stages, ragged_batch);
     if (s.smem_bytes <= kDecodeMaxSmem || s.stages <= 2) break;
   }
 }
@@ -1056,8 +1111,11 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
   DecodeShape s{};
   const int64_t rows = p.heads_q / p.heads_kv * p.seq_q;
   s.D = p.head_dim <= 64 ? 64 : 128;
-  s.NT = rows <= 8 ? 1 : 2;
-  s.HP = 8 * s.NT;
+  // One column tile per pass: two would serve 16 rows with one unpacking, but
+  // leave too few registers for 64-key chunks (1790 ns per unit against twice
+  // 550; the passes' records come out of L2 the second time).
+  s.NT = 1;
+  s.HP = 8;
   s.passes = static_cast<int>((rows + s.HP - 1) / s.HP);
   s.ragged = p.kv_lens != nullptr;
   s.tiles_per_group =
@@ -1066,14 +1124,33 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
                      .tiles;
   if (s.tiles_per_group < 1) s.tiles_per_group = 1;
   s.groups = p.batch * p.heads_kv * s.passes;
-  s.units = s.groups * s.tiles_per_group;
-  s.grid = static_cast<int>(s.units < sm_count ? s.units : sm_count);
+  // One range per CTA, all equal, or (all groups alike) every group cut into
+  // as many as the SMs allow, which saves the changes of groups inside ranges
+  // and, at one range per group, the merge of partials: whichever is shorter
+  // by its longest range.
+  const int64_t real = s.groups * s.tiles_per_group;
+  s.lead = kQ4Lead;
+  s.units = real + s.groups * s.lead;
+  s.grid = static_cast<int>(real < sm_count ? real : sm_count);
+  if (!s.ragged && s.groups > 0 && s.groups <= sm_count) {
+    int64_t split = sm_count / s.groups;
+    if (split > s.tiles_per_group) split = s.tiles_per_group;
+    const double apart = double((s.tiles_per_group + split - 1) / split) * kQ4UnitNs +
+                         (split > 1 ? kQ4MergeNs : 0.0);
+    const double even = double((s.units + sm_count - 1) / sm_count) * kQ4UnitNs + kQ4MergeNs;
+    if (apart <= even) {
+      s.split = static_cast<int>(split);
+      s.lead = 0;
+      s.units = real;
+      s.grid = static_cast<int>(s.groups * split);
+    }
+  }
   if (s.grid < 1) s.grid = 1;
   const int rb = s.ragged ? static_cast<int>(p.batch) : 0;
   if (s.D == 128)
-    s.NT == 1 ? fit<4, 1>(s, rb) : fit<4, 2>(s, rb);
+    fit<4>(s, rb);
   else
-    s.NT == 1 ? fit<2, 1>(s, rb) : fit<2, 2>(s, rb);
+    fit<2>(s, rb);
   const int64_t slots = static_cast<int64_t>(s.grid) * 2 * s.HP;
   int64_t at = kScratchOffset;
   s.zero_counters = s.groups * 4 > kCounterRegionBytes;
@@ -1088,18 +1165,11 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
   return s;
 }
 
-int decode_q4_threads(const DecodeShape& s) {
-  return s.NT == 1 ? Q4Layout<4, 1>::kThreads : Q4Layout<4, 2>::kThreads;
-}
-
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
   const bool f16 = p.dtype == GQA_DTYPE_F16;
-  if (s.D == 128)
-    return s.NT == 1 ? launch_nt<4, 1>(s, a, tmk, tmv, stream, f16)
-                     : launch_nt<4, 2>(s, a, tmk, tmv, stream, f16);
-  return s.NT == 1 ? launch_nt<2, 1>(s, a, tmk, tmv, stream, f16)
-                   : launch_nt<2, 2>(s, a, tmk, tmv, stream, f16);
+  return s.D == 128 ? launch_ng<4>(s, a, tmk, tmv, stream, f16)
+                    : launch_ng<2>(s, a, tmk, tmv, stream, f16);
 }
 
 }  // namespace gqa

@@ -80,6 +80,7 @@ struct DecodeShape {
   int smem_bytes;
   bool ragged;      // per-sequence kv_lens: the partition is computed on the device
   bool zero_counters;  // more groups than the counter region holds: zero them per call
+  int split, lead;  // 4-bit caches: CTAs per group (0: equal ranges), empty places before a group
   int64_t counters_offset, part_o_offset, part_ml_offset;
   int64_t workspace_end;  // bytes of workspace the launch uses
 };
@@ -266,7 +267,12 @@ int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 // Attention over records for single tokens and short query blocks: the shape,
 // arguments (make_decode_args) and workspace of the 16-bit decode.
 DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
-int decode_q4_threads(const DecodeShape& s);
+// Measured times that plans go by (ns): a 128-key unit of one SM, the merge of
+// a split group's partials; and what a change of groups inside a range costs,
+// in units.
+constexpr double kQ4UnitNs = 550, kQ4MergeNs = 2500;
+constexpr int kQ4Lead = 3;
+constexpr int kQ4Threads = 256;
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
 
