@@ -166,7 +166,7 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
   plan->grid = s.grid;
   plan->block = kQ4Threads;
   plan->smem_bytes = s.smem_bytes;
-  plan->launches = s.zero_counters ? 2 : 1;
+  plan->launches = 1 + (s.zero_counters ? 1 : 0) + (p.has_mask ? 1 : 0);
   plan->work_units = static_cast<int32_t>(s.groups * s.tiles_per_group);
   plan->workspace_bytes = (s.workspace_end + 255) / 256 * 256;
   return GQA_OK;
@@ -409,7 +409,7 @@ GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cac
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
-  return launch_decode_q4(p, s, a, tmk, tmv, stream);
+  return launch_decode_q4(p, s, a, ws, tmk, tmv, stream);
 }
 
 }  // extern "C"

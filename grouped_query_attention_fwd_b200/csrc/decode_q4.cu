@@ -59,6 +59,9 @@ constexpr int KT = kDecodeKeysPerTile;
 constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
 constexpr int kFastMerge = 4;              // contributors of a split group merged directly
 constexpr int kBatch = 8;                  // partials loaded at a time by the other merge
+// How many units longer than equal ranges the ranges may be that no two groups
+// share, for ragged batches: what the changes of groups inside a range cost.
+constexpr int kApartUnits = 6;
 
 template <int NG>
 struct Q4Layout {
@@ -79,8 +82,10 @@ struct Q4Layout {
   static constexpr int kRow = D + 4;               // a row's O, then (m, l), padded (floats)
   static constexpr int kScratch = W * HP * kRow * 4;
   static constexpr int kQRows = HP * D * 2;        // Q rows of the range's second group
+  static constexpr int kVis = HP * (KT / 32) * 4;  // a unit's mask bits of the pass's queries
   static int bytes(int stages, int ragged_batch) {
-    return 128 /*alignment slack*/ + stages * kStage + kScratch + kQRows + (2 * stages + 2) * 8 + 32 +
+    return 128 /*alignment slack*/ + stages * (kStage + kVis) + kScratch + kQRows + (2 * stages + 2) * 8 +
+           32 +
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
 };
@@ -131,6 +136,45 @@ __device__ __forceinline__ void load_params(uint32_t (&w)[NG], uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
 }
 
+// 32-bit words of one query's mask bits: whole 128-key units.
+__host__ __device__ constexpr int64_t mask_words(int64_t Sk) { return (Sk + KT - 1) / KT * (KT / 32); }
+
+constexpr int kMaskSpan = 1024;  // keys a warp packs at a time, a word per lane
+
+// The mask as bits, one per key: [batch, seq_q] rows of mask_words.  The decode
+// kernel needs each bit in up to eight heads' passes; read as bytes there, in
+// its producer or its consumers, they cost it more than the records (8 x 6001
+// keys, four queries: 100 and 55 us against 32 without a mask).
+__global__ void __launch_bounds__(256)
+    gqa_q4_mask_bits_kernel(const DecodeArgs a, uint32_t* __restrict__ bits) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t words = mask_words(a.Sk);
+  const int64_t k0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kMaskSpan;
+  if (k0 >= a.Sk) return;
+  for (int64_t row = blockIdx.y; row < static_cast<int64_t>(a.B) * a.Sq; row += gridDim.y) {
+    const int64_t b = row / a.Sq, i = row - b * a.Sq;
+    const uint8_t* m = a.mask + b * a.ms[0] + i * a.ms[1];
+    uint32_t mine = 0u;
+#pragma unroll
+    for (int w0 = 0; w0 < 32; w0 += 8) {
+      uint8_t on[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const int64_t key = k0 + 32 * (w0 + w) + lane;
+        on[w] = key < a.Sk ? __ldg(m + key) : 0;
+      }
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const uint32_t word = __ballot_sync(0xffffffffu, on[w] != 0);
+        if (lane == w0 + w) mine = word;
+      }
+    }
+    if (k0 / 32 + lane < words) bits[row * words + k0 / 32 + lane] = mine;
+  }
+}
+
 // MQ: several query positions per kv head; row r = head * seq_q + query.
 template <int NG, bool MQ, bool F16>
 __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
@@ -138,6 +182,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
                          const __grid_constant__ CUtensorMap tmv, const DecodeArgs a,
                          const int tiles_per_group, const int passes, const int units,
                          const int stages, const int split, const int lead,
+                         const uint32_t* __restrict__ mask_bits,
                          uint32_t* __restrict__ counters) {
   using L = Q4Layout<NG>;
   constexpr int HP = L::HP, D = L::D, W = L::W, P = L::kPitch, R = L::kRow;
@@ -149,7 +194,8 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
                                              ~static_cast<uintptr_t>(127));
   float* scr = reinterpret_cast<float*>(ring + stages * L::kStage);
   uint16_t* q_next = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(scr) + L::kScratch);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(q_next) + L::kQRows);
+  uint32_t* vis_s = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(q_next) + L::kQRows);
+  uint64_t* full = reinterpret_cast<uint64_t*>(vis_s + stages * (L::kVis / 4));
   uint64_t* empty = full + stages;
   uint64_t* q_full = empty + stages;     // the second group's Q rows landed
   uint64_t* scr_free = q_full + 1;       // the scratch's states have been merged
@@ -162,6 +208,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
   constexpr uint32_t kNoPeek = 0xFFFFFFFFu;
   int* flushed = const_cast<int*>(abort_flag) + 4;  // warps whose state of a mid group is in the scratch
   volatile int* mid_last = abort_flag + 5;  // the range's first group is this CTA's to merge
+  volatile int* piece = abort_flag + 6;     // ragged, every group in ranges of its own: most units of one
   int* len_s = const_cast<int*>(abort_flag) + 8;
   int* pre_s = len_s + a.B;
 
@@ -212,15 +259,44 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
     }
     __syncthreads();
     if (warp == 0) {
-      // pre[b + 1] = sum over entries <= b of (groups per entry) x (places of a group).
+      auto tiles_of = [&](int b) {
+        return decode_key_range(len_s[b], a.Sk, a.Sq, a.causal, a.causal_offset, a.window).tiles;
+      };
+      // Every group in ranges of its own (see below): the fewest units per
+      // range with which they are no more than the CTAs.
+      int units_of_piece = 0;
+      const int grid = static_cast<int>(gridDim.x);
+      if (a.B <= grid / gpb) {
+        int most = 0, all = 0;
+        for (int b = lane; b < a.B; b += 32) {
+          const int t = tiles_of(b);
+          most = max(most, t);
+          all += t;
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        all = __reduce_add_sync(0xffffffffu, all);
+        int lo = 1, hi = most;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          int n = 0;
+          for (int b = lane; b < a.B; b += 32) n += (tiles_of(b) + mid - 1) / mid;
+          n = __reduce_add_sync(0xffffffffu, n);
+          if (n <= grid / gpb)
+            hi = mid;
+          else
+            lo = mid + 1;
+        }
+        if (lo <= (all + lead * a.B) / (grid / gpb) + kApartUnits) units_of_piece = lo;
+      }
+      if (lane == 0) *piece = units_of_piece;
+      // pre[b + 1] = sum over entries <= b of their places (or ranges).
       int carry = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
         int v = 0;
         if (b < a.B)
-          v = gpb * (lead + decode_key_range(len_s[b], a.Sk, a.Sq, a.causal, a.causal_offset,
-                                             a.window)
-                                .tiles);
+          v = gpb * (units_of_piece > 0 ? (tiles_of(b) + units_of_piece - 1) / units_of_piece
+                                        : lead + tiles_of(b));
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int n = __shfl_up_sync(0xffffffffu, v, o);
@@ -241,31 +317,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
   sc.total = ragged ? pre_s[a.B] : units;
   sc.P = static_cast<int>(gridDim.x) < sc.total ? static_cast<int>(gridDim.x) : sc.total;
 
-  // The places of a launch: every group has `lead` empty ones (what a change
-  // of groups costs, in units) and then one per unit.  They are cut into one
-  // range per CTA, all equal; or, with `split`, every group into `split` equal
-  // ranges and none shared by two groups (no lead then).
-  auto start_of = [&](int cta) {
-    if (split > 0)
-      return cta / split * tiles_per_group + cta % split * tiles_per_group / split;
-    return range_start(cta, sc.total, sc.P);
-  };
-  auto cta_of = [&](int place) {
-    if (split > 0) {
-      const int g = place / tiles_per_group, r = place - g * tiles_per_group;
-      return g * split + ((r + 1) * split + tiles_per_group - 1) / tiles_per_group - 1;
-    }
-    return cta_of_unit(place, sc.total, sc.P);
-  };
   Cursor cu;
-  auto seek_entry = [&](int place) {  // the cursor at the entry of a place
-    if (cu.b >= 0 && place >= cu.beg && place < cu.end) return;
-    cu.b = sc.batch_of(place);
-    cu.beg = sc.start_of(cu.b);
-    cu.kr = decode_key_range(sc.len ? sc.len[cu.b] : a.Sk, a.Sk, a.Sq, a.causal, a.causal_offset,
-                             a.window);
-    cu.end = cu.beg + gpb * (cu.kr.tiles + lead);
-  };
   // Address of row hl (a head, or a (head, query) pair) of kv head kv of entry b.
   auto q_row = [&](int b, int kv, int hl) {
     const int hh = MQ ? hl / a.Sq : hl, qi = MQ ? hl % a.Sq : 0;
@@ -277,30 +329,81 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
   struct Group {
     int b, kv, pass, id, beg, tiles, c_lo, c_hi, rows;
   };
-  auto id_at = [&](int place) {
-    seek_entry(place);
-    return cu.b * gpb + (place - cu.beg) / (cu.kr.tiles + lead);
-  };
-  auto group_at = [&](int place) {
+  auto group_of_entry = [&](int gi) {  // the cursor's entry
     Group g;
-    g.id = id_at(place);
+    g.id = cu.b * gpb + gi;
     g.b = cu.b;
-    const int gi = g.id - cu.b * gpb;
     g.kv = gi / passes;
     g.pass = gi - g.kv * passes;
-    g.beg = cu.beg + gi * (cu.kr.tiles + lead) + lead;
     g.tiles = cu.kr.tiles;
-    g.c_lo = cta_of(g.beg);
-    g.c_hi = cta_of(g.beg + g.tiles - 1);
     g.rows = min(HP, a.rows - g.pass * HP);
     return g;
   };
-  const bool has_range = static_cast<int>(blockIdx.x) < sc.P;
-  const int v_begin = has_range ? start_of(blockIdx.x) : 0;
-  int v_end = has_range ? start_of(blockIdx.x + 1) : 0;
-  if (v_begin < v_end) {  // a range that ends in a group's lead has no unit of that group
-    const Group g = group_at(v_end - 1);
-    if (v_end <= g.beg) v_end = max(v_begin, g.beg - lead);
+  auto range_of_entry = [&](int b) {
+    return decode_key_range(sc.len ? sc.len[b] : a.Sk, a.Sk, a.Sq, a.causal, a.causal_offset,
+                            a.window);
+  };
+  // The units of a launch are cut into CTA ranges in one of two ways.
+  //  apart: every group has ranges of its own, `split` of them (uniform), or
+  //    as many as keep each within `piece` units (ragged).  No CTA changes
+  //    groups.  A place is a unit of the CTA's own group.
+  //  even: all groups lie end to end and are cut into equal ranges.  Every
+  //    group has `lead` empty places (what a change of groups costs, in units)
+  //    and then one per unit.
+  const bool apart = ragged ? *piece > 0 : split > 0;
+  auto id_at = [&](int place) {  // even: the group of a place; the cursor goes to its entry
+    if (cu.b < 0 || place < cu.beg || place >= cu.end) {
+      cu.b = sc.batch_of(place);
+      cu.beg = sc.start_of(cu.b);
+      cu.kr = range_of_entry(cu.b);
+      cu.end = cu.beg + gpb * (cu.kr.tiles + lead);
+    }
+    return cu.b * gpb + (place - cu.beg) / (cu.kr.tiles + lead);
+  };
+  Group own{};  // apart: the CTA's group
+  auto group_at = [&](int place) {
+    if (apart) return own;
+    const int id = id_at(place);
+    Group g = group_of_entry(id - cu.b * gpb);
+    g.beg = cu.beg + (id - cu.b * gpb) * (cu.kr.tiles + lead) + lead;
+    g.c_lo = cta_of_unit(g.beg, sc.total, sc.P);
+    g.c_hi = cta_of_unit(g.beg + g.tiles - 1, sc.total, sc.P);
+    return g;
+  };
+  const int cta = static_cast<int>(blockIdx.x);
+  int v_begin = 0, v_end = 0;  // this CTA's places
+  if (cta < sc.P) {
+    if (apart) {
+      int gi, part, parts;
+      if (ragged) {
+        cu.b = sc.batch_of(cta);
+        cu.kr = range_of_entry(cu.b);
+        parts = (cu.kr.tiles + *piece - 1) / *piece;
+        const int r = cta - sc.start_of(cu.b);
+        gi = r / parts;
+        part = r - gi * parts;
+      } else {
+        parts = split;
+        const int id = cta / split;
+        part = cta - id * split;
+        cu.b = id / gpb;
+        gi = id - cu.b * gpb;
+        cu.kr = range_of_entry(cu.b);
+      }
+      own = group_of_entry(gi);
+      own.beg = 0;
+      own.c_lo = cta - part;
+      own.c_hi = own.c_lo + parts - 1;
+      v_begin = static_cast<int>(static_cast<int64_t>(part) * own.tiles / parts);
+      v_end = static_cast<int>(static_cast<int64_t>(part + 1) * own.tiles / parts);
+    } else {
+      v_begin = range_start(cta, sc.total, sc.P);
+      v_end = range_start(cta + 1, sc.total, sc.P);
+      if (v_begin < v_end) {  // a range that ends in a group's lead has no unit of that group
+        const Group g = group_at(v_end - 1);
+        if (v_end <= g.beg) v_end = max(v_begin, g.beg - lead);
+      }
+    }
   }
 
   if (warp == W) {
@@ -325,6 +428,14 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
       const int t0 = max(va - grp.beg, 0);               // units [t0, t1) of the group
       const int t1 = min(v_end - grp.beg, grp.tiles);
       const int kv = grp.kv, b = grp.b;
+      // With a mask: this lane's query of the pass (they go in row order,
+      // wrapping) and its bits.
+      const uint32_t* my_bits = nullptr;
+      if (a.has_mask && lane / (KT / 32) < (MQ ? min(a.Sq, HP) : 1)) {
+        const int qi = MQ ? (grp.pass * HP + lane / (KT / 32)) % a.Sq : 0;
+        my_bits = mask_bits + (static_cast<int64_t>(b) * a.Sq + qi) * mask_words(a.Sk) +
+                  lane % (KT / 32);
+      }
       int key0 = (t0 + cu.kr.t0) * KT;
       if (va == v_begin && !ragged) {
         // Contiguous caches: the first units start towards L2 before the grid
@@ -363,11 +474,15 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
               row[h] = __shfl_sync(0xffffffffu, my_row, 2 * i + h);
             }
           }
+          // Mask bits of the unit's 128 keys, lane 4 i + w: query i of the pass,
+          // keys 32 w .. + 31.  (Read before the wait for a free stage.)
+          const uint32_t bits = my_bits != nullptr ? __ldg(my_bits + key0 / 32) : 0u;
           // (Every lane waits: the warp stays converged.)
           ok = __all_sync(0xffffffffu, mbar_try_wait(&empty[s], parity) ||
                                            mbar_wait(&empty[s], parity, abort_flag, a.err,
                                                      kErrDecodeWait, a.wait_ns));
-          if (ok && grp.beg - lead * (grp.id + 1) + u == a.withhold_unit) {
+          if (ok && (apart ? grp.id * tiles_per_group : grp.beg - lead * (grp.id + 1)) + u ==
+                        a.withhold_unit) {
             // Test of the bounded waits, as in the 16-bit decode: nothing more
             // is issued, and the consumers' wait for this unit runs out.
             const uint64_t t0 = globaltimer_ns();
@@ -377,6 +492,10 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
             ok = false;
           }
           if (!ok) break;
+          if (a.has_mask) {
+            vis_s[s * (L::kVis / 4) + lane] = bits;
+            __syncwarp();  // (lane 0's arrival below releases them)
+          }
           if (lane == 0) {
             uint8_t* st = ring + s * L::kStage;
             mbar_arrive_expect_tx(&full[s], L::kStage);
@@ -462,7 +581,8 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
     // Partial slot of a CTA for a split group: only a range's first and last
     // group can be split, so there are two.
     auto slot_of = [&](int cta, int id) {
-      return (cta * 2 + (id_at(start_of(cta)) == id ? 0 : 1)) * HP;
+      if (apart) return cta * 2 * HP;
+      return (cta * 2 + (id_at(range_start(cta, sc.total, sc.P)) == id ? 0 : 1)) * HP;
     };
     // All partials of a split group are published: their merge by the whole
     // consumer group, eight contributors' loads in flight at a time.
@@ -622,11 +742,11 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
           all_lo = static_cast<int>(lo < 0 ? 0 : (lo < len ? lo : len));
         }
       }
-      // With a mask: the pass's queries, in row order from qi0 (wrapping), and
-      // which of them this thread's rows are.
-      const int nq = MQ ? min(a.Sq, HP) : 1;
-      const int qi0 = MQ ? pass * HP % a.Sq : 0;
-      auto query_of = [&](int e) { return !MQ ? 0 : (a.Sq < HP ? (2 * c + e) % a.Sq : 2 * c + e); };
+      // With a mask: where the bits of this thread's two rows' queries are.
+      int vis_at[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        vis_at[e] = (!MQ ? 0 : (a.Sq < HP ? (2 * c + e) % a.Sq : 2 * c + e)) * (KT / 32);
 
       float o[NG][2][4], corr[NG][2];
       float osum[4];  // fp16: lanes 4 t + c hold group t's summed weights
@@ -661,55 +781,30 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
           }
         const int chunk = x % kChunks;
         const int key0 = (t0 + kr.t0 + it - done) * KT + chunk * kChunk;
+        const bool landed =
+            mbar_try_wait(&full[s], parity) ||
+            mbar_wait(&full[s], parity, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
+        if (a.trace != nullptr && x == 0 && lane == 0) trace()[kTrFirstLand] = globaltimer_ns();
         // Visible keys of the chunk, one bit each, where some are not: the
-        // range of each row, and the mask's bytes of each query, a key per
-        // lane, gathered by a ballot.
+        // range of each row, and its query's mask bits.
         uint32_t vis[2][NW];
         bool whole = key0 >= all_lo && key0 + kChunk <= all_hi;
         bool none = key0 >= kr.hi || key0 + kChunk <= kr.lo;
         if (!none && (!whole || a.has_mask)) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int w = 0; w < NW; ++w)
-              vis[e][w] = below(vhi[e] - key0 - 32 * w) & ~below(vlo[e] - key0 - 32 * w);
-          if (a.has_mask) {
-            uint32_t on[2][NW];
-#pragma unroll
-            for (int w = 0; w < NW; ++w) on[0][w] = on[1][w] = 0u;
-#pragma unroll 4
-            for (int i = 0; i < nq; ++i) {
-              const int qi = qi0 + i < a.Sq ? qi0 + i : qi0 + i - a.Sq;
-              const uint8_t* row = a.mask + b * a.ms[0] + static_cast<int64_t>(qi) * a.ms[1];
-#pragma unroll
-              for (int w = 0; w < NW; ++w) {
-                const int key = key0 + 32 * w + lane;
-                const uint32_t bits = __ballot_sync(0xffffffffu, key < kr.hi && row[key] != 0);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  if (!MQ || query_of(e) == i) on[e][w] = bits;
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int w = 0; w < NW; ++w) vis[e][w] &= on[e][w];
-          }
+          const uint32_t* words = vis_s + s * (L::kVis / 4) + chunk * NW;
           uint32_t all = ~0u, any = 0u;
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
+              vis[e][w] = below(vhi[e] - key0 - 32 * w) & ~below(vlo[e] - key0 - 32 * w);
+              if (a.has_mask) vis[e][w] &= words[vis_at[e] + w];
               all &= vis[e][w];
               any |= vis[e][w];
             }
           whole = __all_sync(0xffffffffu, all == ~0u);
           none = !__any_sync(0xffffffffu, any != 0u);
         }
-        const bool landed =
-            mbar_try_wait(&full[s], parity) ||
-            mbar_wait(&full[s], parity, abort_flag, a.err, kErrDecodeWait, a.wait_ns);
-        if (a.trace != nullptr && x == 0 && lane == 0) trace()[kTrFirstLand] = globaltimer_ns();
         // (A wait that gave up sets the abort flag: the arithmetic is skipped,
         // the walk goes on, so that all warps reach the same barriers.)
         if (!__all_sync(0xffffffffu, landed) || none) {
@@ -1061,8 +1156,8 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
 }
 
 template <int NG, bool MQ, bool F16>
-int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
-             const CUtensorMap& tmv, cudaStream_t stream) {
+int launch_t(const DecodeShape& s, const DecodeArgs& a, const uint32_t* mask_bits,
+             const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
   auto kern = gqa_decode_q4_kernel<NG, MQ, F16>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem_bytes) !=
       cudaSuccess) {
@@ -1080,7 +1175,7 @@ int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, kern, tmk, tmv, a, s.tiles_per_group, s.passes,
-                         static_cast<int>(s.units), s.stages, s.split, s.lead, a.counters) != cudaSuccess) {
+                         static_cast<int>(s.units), s.stages, s.split, s.lead, mask_bits, a.counters) != cudaSuccess) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }
@@ -1088,13 +1183,13 @@ int launch_t(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
 }
 
 template <int NG>
-int launch_ng(const DecodeShape& s, const DecodeArgs& a, const CUtensorMap& tmk,
-              const CUtensorMap& tmv, cudaStream_t stream, bool f16) {
+int launch_ng(const DecodeShape& s, const DecodeArgs& a, const uint32_t* mask_bits,
+              const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream, bool f16) {
   if (a.Sq > 1)
-    return f16 ? launch_t<NG, true, true>(s, a, tmk, tmv, stream)
-               : launch_t<NG, true, false>(s, a, tmk, tmv, stream);
-  return f16 ? launch_t<NG, false, true>(s, a, tmk, tmv, stream)
-             : launch_t<NG, false, false>(s, a, tmk, tmv, stream);
+    return f16 ? launch_t<NG, true, true>(s, a, mask_bits, tmk, tmv, stream)
+               : launch_t<NG, true, false>(s, a, mask_bits, tmk, tmv, stream);
+  return f16 ? launch_t<NG, false, true>(s, a, mask_bits, tmk, tmv, stream)
+             : launch_t<NG, false, false>(s, a, mask_bits, tmk, tmv, stream);
 }
 
 template <int NG>
@@ -1161,15 +1256,37 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
   }
   s.part_ml_offset = at;
   s.part_o_offset = s.part_ml_offset + ((slots * 8 + 255) / 256) * 256;
-  s.workspace_end = s.part_o_offset + slots * s.D * 4;
+  s.mask_offset = s.part_o_offset + slots * s.D * 4;  // (a multiple of 256)
+  s.workspace_end =
+      s.mask_offset + (p.has_mask ? p.batch * p.seq_q * mask_words(p.seq_k) * 4 : 0);
   return s;
 }
 
-int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
+int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
+  uint32_t* bits = nullptr;
+  if (a.has_mask) {
+    bits = reinterpret_cast<uint32_t*>(ws + s.mask_offset);
+    const int64_t rows = p.batch * p.seq_q;
+    const int64_t spans = (p.seq_k + kMaskSpan - 1) / kMaskSpan;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((spans + 7) / 8),
+                       static_cast<unsigned>(rows < 65535 ? rows : 65535));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, gqa_q4_mask_bits_kernel, a, bits) != cudaSuccess) {
+      cudaGetLastError();
+      return GQA_ERR_CUDA;
+    }
+  }
   const bool f16 = p.dtype == GQA_DTYPE_F16;
-  return s.D == 128 ? launch_ng<4>(s, a, tmk, tmv, stream, f16)
-                    : launch_ng<2>(s, a, tmk, tmv, stream, f16);
+  return s.D == 128 ? launch_ng<4>(s, a, bits, tmk, tmv, stream, f16)
+                    : launch_ng<2>(s, a, bits, tmk, tmv, stream, f16);
 }
 
 }  // namespace gqa

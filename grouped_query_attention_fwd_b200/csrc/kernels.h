@@ -81,6 +81,7 @@ struct DecodeShape {
   bool ragged;      // per-sequence kv_lens: the partition is computed on the device
   bool zero_counters;  // more groups than the counter region holds: zero them per call
   int split, lead;  // 4-bit caches: CTAs per group (0: equal ranges), empty places before a group
+  int64_t mask_offset;  // 4-bit caches: the mask as bits
   int64_t counters_offset, part_o_offset, part_ml_offset;
   int64_t workspace_end;  // bytes of workspace the launch uses
 };
@@ -273,7 +274,7 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
 constexpr double kQ4UnitNs = 550, kQ4MergeNs = 2500;
 constexpr int kQ4Lead = 3;
 constexpr int kQ4Threads = 256;
-int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a,
+int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
 
 // ------------------------------------------------------------ fill: zeros (seq_k == 0) or NaN

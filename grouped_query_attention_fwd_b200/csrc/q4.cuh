@@ -37,11 +37,13 @@ __device__ __forceinline__ uint32_t to_16(float x) {
 // Scale and minimum of a group from its 4 bytes in the record's head.
 template <bool F16>
 __device__ __forceinline__ float scale_of(uint32_t word) {
-  return to_f32<F16>(word & 0xFFFFu);
+  if (F16) return __low2float(*reinterpret_cast<const __half2*>(&word));
+  return __uint_as_float(word << 16);
 }
 template <bool F16>
 __device__ __forceinline__ float min_of(uint32_t word) {
-  return to_f32<F16>(word >> 16);
+  if (F16) return __high2float(*reinterpret_cast<const __half2*>(&word));
+  return __uint_as_float(word & 0xFFFF0000u);
 }
 
 }  // namespace q4
