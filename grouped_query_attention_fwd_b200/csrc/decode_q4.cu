@@ -67,11 +67,11 @@ template <int NG>
 struct Q4Layout {
   static constexpr int D = NG * kGroup;            // head_dim, padded
   static constexpr int HP = 8;                     // rows per pass: the columns of one MMA
-  static constexpr int W = 7;                      // consumer warps: with the producer two per scheduler
+  static constexpr int W = 11;                     // consumer warps: with the producer three per scheduler
   // 16-key MMA tiles a warp takes at a time: more of them share the waits,
-  // votes and address arithmetic of a chunk (16, 32 and 64 keys took 754, 610
-  // and 560 ns per unit of an SM).
-  static constexpr int kSub = 4;
+  // votes and address arithmetic of a chunk (one takes a quarter longer), and
+  // four, with 7 warps for their registers, gain nothing over two.
+  static constexpr int kSub = 2;
   static constexpr int kChunk = 16 * kSub;         // keys of a chunk
   static constexpr int kChunks = KT / kChunk;
   static constexpr int kThreads = (W + 1) * 32;

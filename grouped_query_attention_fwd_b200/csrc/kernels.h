@@ -272,8 +272,8 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
 // a split group's partials; and what a change of groups inside a range costs,
 // in units.
 constexpr double kQ4UnitNs = 550, kQ4MergeNs = 2500;
-constexpr int kQ4Lead = 3;
-constexpr int kQ4Threads = 256;
+constexpr int kQ4Lead = 6;
+constexpr int kQ4Threads = 384;
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
 

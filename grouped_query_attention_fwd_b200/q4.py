@@ -71,12 +71,24 @@ def _remember(seen, key, value):
 
 
 def _like(t):
-    """What the checks see of a tensor (or None)."""
-    return None if t is None else (t.dtype, t.shape, t.stride(), t.get_device())
+    """What the checks see of a tensor."""
+    return t.dtype, t.shape, t.stride(), t.get_device()
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+# torch's functions that every call needs (filled in by the first call: torch is
+# imported no earlier than a tensor exists).
+_device_now = _stream_now = _capturing = None
+
+
+def _bind_torch():
+    global _device_now, _stream_now, _capturing
+    c = _torch()._C
+    _device_now, _stream_now = c._cuda_getDevice, c._cuda_getCurrentRawStream
+    _capturing = c._cuda_isCurrentStreamCapturing
 
 
 def q4_record_bytes(head_dim: int) -> int:
@@ -116,9 +128,10 @@ def _check_devices(idx, *tensors):
 def _elsewhere(idx, stream):
     """Contexts that make device ``idx`` and ``stream`` current, or None where
     they are (the usual case)."""
-    c = _torch()._C
-    if idx < 0 or (c._cuda_getDevice() == idx and
-                   (stream is None or int(stream) == c._cuda_getCurrentRawStream(idx))):
+    if _device_now is None:
+        _bind_torch()
+    if idx < 0 or (_device_now() == idx and
+                   (stream is None or int(stream) == _stream_now(idx))):
         return None
     torch = _torch()
     stack = contextlib.ExitStack()
@@ -137,14 +150,14 @@ def _workspace(idx, stream, nbytes, workspace):
     graphs replayed side by side never share one."""
     if workspace is not None:
         return workspace
-    torch = _torch()
-    if torch._C._cuda_isCurrentStreamCapturing():
+    if _capturing():
+        torch = _torch()
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
         ws[:_HEAD].zero_()
         return ws
     ws = _workspaces.get((idx, stream))
     if ws is None or ws.numel() < nbytes:
-        ws = workspace_for(torch.device("cuda", idx), nbytes, stream)
+        ws = workspace_for(_torch().device("cuda", idx), nbytes, stream)
     return ws
 
 
@@ -198,7 +211,8 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
             return kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens, advance,
                                 workspace, None, block_table)
     key = (_like(k_new), _like(v_new), _like(cache_k), _like(cache_v), _like(kv_lens),
-           _like(new_lens), _like(block_table), advance)
+           None if new_lens is None else _like(new_lens),
+           None if block_table is None else _like(block_table), advance)
     seen = _known("append")
     d = seen.get(key)
     if d is None:
@@ -215,7 +229,7 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
                                             k_new.shape[3], block_table, bool(advance)))
     d.block_table = _ptr(block_table)
     d.counts = _ptr(new_lens)
-    handle = _torch()._C._cuda_getCurrentRawStream(idx)
+    handle = _stream_now(idx)
     ws = _workspace(idx, handle, 256, workspace)
     rc = _lib.gqa_kv_append_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k_new.data_ptr(),
                                v_new.data_ptr(), kv_lens.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -241,7 +255,9 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
     starts = start if isinstance(start, torch.Tensor) else None
     start = 0 if starts is not None else int(start)
     key = (dtype, head_dim, n, start if n is None else None, _like(cache_k), _like(cache_v),
-           _like(kv_lens), _like(starts), _like(out_k), _like(out_v), _like(block_table))
+           None if kv_lens is None else _like(kv_lens), None if starts is None else _like(starts),
+           None if out_k is None else _like(out_k), None if out_v is None else _like(out_v),
+           None if block_table is None else _like(block_table))
     seen = _known("read")
     known = seen.get(key)
     if known is None:
@@ -266,12 +282,16 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
             dtype, cache_k, cache_v, fresh if out_k is None else out_k,
             fresh if out_v is None else out_v, shape[3], block_table, False)))
     shape, d = known
-    k = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_k is None else out_k
-    v = torch.empty(shape, dtype=dtype, device=cache_k.device) if out_v is None else out_v
+    k, v = out_k, out_v
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache_k.device)
+    if v is None:
+        v = torch.empty_like(k) if out_k is None else torch.empty(shape, dtype=dtype,
+                                                                  device=cache_k.device)
     d.block_table = _ptr(block_table)
     d.starts = _ptr(starts)
     d.start = start
-    handle = torch._C._cuda_getCurrentRawStream(idx)
+    handle = _stream_now(idx)
     ws = _workspace(idx, handle, 256, workspace)
     rc = _lib.gqa_kv_read_q4(d, cache_k.data_ptr(), cache_v.data_ptr(), k.data_ptr(),
                              v.data_ptr(), _ptr(kv_lens), ws.data_ptr(), ws.numel(), handle)
@@ -349,8 +369,10 @@ def forward_q4(q, cache_k, cache_v, mask=None, causal=False, scale=None, out=Non
         with away:
             return forward_q4(q, cache_k, cache_v, mask, causal, scale, out, workspace, None,
                               causal_offset, window, kv_lens, block_table)
-    key = (_like(q), _like(cache_k), _like(cache_v), _like(mask), _like(kv_lens),
-           _like(block_table), _like(out), causal, scale, causal_offset, window)
+    key = (_like(q), _like(cache_k), _like(cache_v), None if mask is None else _like(mask),
+           None if kv_lens is None else _like(kv_lens),
+           None if block_table is None else _like(block_table),
+           None if out is None else _like(out), causal, scale, causal_offset, window)
     seen = _known("forward")
     known = seen.get(key)
     if known is None:
@@ -361,13 +383,14 @@ def forward_q4(q, cache_k, cache_v, mask=None, causal=False, scale=None, out=Non
         _check_int32(kv_lens, q.shape[0], "kv_lens")
         p = q4_problem_for(q, cache_k, cache_v, mask, causal, scale, out, causal_offset, window,
                            kv_lens, block_table)
-        known = _remember(seen, key, (p, _query(p).workspace_bytes))
-    p, nbytes = known
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        known = _remember(seen, key, (p, _query(p).workspace_bytes, q.is_contiguous()))
+    p, nbytes, contiguous = known
+    if out is None:  # [B, Hq, Sq, D] laid out afresh, whatever q's strides
+        out = torch.empty_like(q) if contiguous else torch.empty(q.shape, dtype=q.dtype,
+                                                                 device=q.device)
     p.kv_lens = _ptr(kv_lens)
     p.block_table = _ptr(block_table)
-    handle = torch._C._cuda_getCurrentRawStream(idx)
+    handle = _stream_now(idx)
     ws = _workspace(idx, handle, nbytes, workspace)
     rc = _lib.gqa_forward_q4(p, q.data_ptr(), cache_k.data_ptr(), cache_v.data_ptr(), _ptr(mask),
                              out.data_ptr(), ws.data_ptr(), ws.numel(), handle)
