@@ -42,7 +42,7 @@ GQA_ERR_SCRATCH_LIMIT, GQA_ERR_KV_LENGTH, GQA_ERR_PAGE = 10, 11, 12
 STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 GQA_DTYPE_BF16, GQA_DTYPE_F32, GQA_DTYPE_F16 = 0, 1, 2
 KERNEL_NAMES = {0: "none", 1: "decode", 2: "prefill", 3: "f32", 4: "zero", 5: "nan", 6: "q4",
-                7: "q4_prefill"}
+                7: "q4_prefill", 8: "q4_chunk"}
 
 EXPORTS = ("gqa_query", "gqa_forward", "gqa_device_status", "gqa_status_string", "gqa_version",
            "gqa_forward_decode_noalloc", "gqa_kv_append", "gqa_debug_decode_trace",

@@ -294,6 +294,13 @@ int encode_decode_kv_map(CUtensorMap* map, const void* base, const gqa_problem& 
                          kDecodeKeysPerTile, 1, f16);
 }
 
+int encode_q_map(CUtensorMap* map, const void* q, const gqa_problem& p, int qpt) {
+  return encode_half_map(map, q, p.batch, p.heads_q, p.seq_q, p.head_dim, p.q_stride,
+                         static_cast<uint32_t>(qpt),
+                         static_cast<uint32_t>(p.heads_q / p.heads_kv),
+                         p.dtype == GQA_DTYPE_F16);
+}
+
 // Prefill of a validated problem: tensor maps, arguments and launches.
 int launch_prefill_call(const gqa_problem& p, int sms, const void* q, const void* k, const void* v,
                         const uint8_t* mask, void* out, uint8_t* ws, cudaStream_t stream) {

@@ -18,6 +18,8 @@ constexpr int64_t kLim = int64_t(1) << 31;
 // a key tile of the two-tile prefill; bytes read and written by the read back.
 constexpr double kDecodeNs = 10000;
 constexpr double kSliceNs = 12000, kTwoTileNs = 2200, kReadBytesPerNs = 4500;
+// Launches and ends of the 128-row kernel, and a key tile of one of its SMs.
+constexpr double kChunkNs = 14000, kChunkTileNs = 1000;
 
 bool aligned(const void* ptr, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
@@ -118,15 +120,28 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
   return s;
 }
 
-// Estimated time of the decode kernel over the same problem.
+// Estimated times of the other two ways over the same problem.
 double decode_ns(const DecodeShape& s, int sms) {
   return kDecodeNs + double(s.units) / sms * kQ4UnitNs;
 }
 
-// Query blocks of up to 8 rows per kv head take one pass over the records;
-// longer ones take a pass per 8 rows, or go over 16-bit scratch.
-bool use_slices(const gqa_problem& p, const DecodeShape& d, const SlicePlan& s, int sms) {
-  return d.passes > 1 && p.seq_q > 1 && s.ns < decode_ns(d, sms);
+double chunk_ns(const ChunkShape& s, int sms) {
+  return kChunkNs + double(s.places) / sms * kChunkTileNs;
+}
+
+// The way to attend: a pass over the records per 8 rows of a kv head (one pass
+// where it has no more), 128-row tiles that unpack each record once, or the
+// two-tile prefill over 16-bit scratch.
+int pick_way(const gqa_problem& p, const DecodeShape& d, const ChunkShape& c, const SlicePlan& s,
+             int sms) {
+  if (d.passes <= 1 || p.seq_q <= 1) return GQA_KERNEL_Q4;
+  double best = decode_ns(d, sms);
+  int way = GQA_KERNEL_Q4;
+  if (c.fits && chunk_ns(c, sms) < best) {
+    best = chunk_ns(c, sms);
+    way = GQA_KERNEL_Q4_CHUNK;
+  }
+  return s.ns < best ? GQA_KERNEL_Q4_PREFILL : way;
 }
 
 int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
@@ -149,10 +164,20 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
     return GQA_OK;
   }
   const DecodeShape s = plan_decode_q4(p, sm_count);
+  const ChunkShape c = plan_chunk_q4(p, sm_count);
   const SlicePlan sl = plan_slices(p, sm_count);
-  if (use_slices(p, s, sl, sm_count)) {
+  plan->kernel = pick_way(p, s, c, sl, sm_count);
+  if (plan->kernel == GQA_KERNEL_Q4_CHUNK) {
+    plan->grid = c.grid;
+    plan->block = kChunkThreads;
+    plan->smem_bytes = c.smem_bytes;
+    plan->launches = 2;
+    plan->work_units = static_cast<int32_t>(c.groups * c.tiles);
+    plan->workspace_bytes = (c.workspace_end + 255) / 256 * 256;
+    return GQA_OK;
+  }
+  if (plan->kernel == GQA_KERNEL_Q4_PREFILL) {
     const PrefillShape f = plan_prefill(slice_problem(p, 0, sl.nb, sl.nh), sm_count);
-    plan->kernel = GQA_KERNEL_Q4_PREFILL;
     plan->grid = f.grid;
     plan->block = kPrefillThreads;
     plan->smem_bytes = f.smem_bytes;
@@ -162,7 +187,6 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
     return GQA_OK;
   }
   if (s.units >= kLim) return GQA_ERR_UNSUPPORTED;  // 32-bit unit indices
-  plan->kernel = GQA_KERNEL_Q4;
   plan->grid = s.grid;
   plan->block = kQ4Threads;
   plan->smem_bytes = s.smem_bytes;
@@ -401,6 +425,29 @@ GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cac
   if (erc != GQA_OK) return erc;
   erc = encode_records(&tmv, cache_v, p, p.v_stride, s.D);
   if (erc != GQA_OK) return erc;
+  if (plan.kernel == GQA_KERNEL_Q4_CHUNK) {
+    const ChunkShape c = plan_chunk_q4(p, sms);
+    CUtensorMap tmq;
+    erc = encode_q_map(&tmq, q, p, c.qpt);
+    if (erc != GQA_OK) return erc;
+    PrefillArgs f{};
+    f.out = static_cast<uint16_t*>(out);
+    for (int d = 0; d < 4; ++d) f.os[d] = p.o_stride[d];
+    f.err = reinterpret_cast<uint32_t*>(ws);
+    f.lens = p.kv_lens;
+    f.Dv = static_cast<int>(p.head_dim);
+    f.B = static_cast<int>(p.batch);
+    f.Hq = static_cast<int>(p.heads_q);
+    f.Hkv = static_cast<int>(p.heads_kv);
+    f.Sq = static_cast<int>(p.seq_q);
+    f.Sk = static_cast<int>(p.seq_k);
+    f.g = static_cast<int>(p.heads_q / p.heads_kv);
+    f.causal = p.causal;
+    f.causal_offset = p.causal_offset;
+    f.window = p.window;
+    f.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634073599);
+    return launch_chunk_q4(p, c, f, ws, tmq, tmk, tmv, stream);
+  }
   const DecodeArgs a = make_decode_args(p, s, q, mask, out, ws);
   // The ticket counters must start at zero; past their region of the
   // workspace other calls may have left bytes.

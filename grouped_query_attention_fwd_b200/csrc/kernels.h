@@ -277,6 +277,33 @@ constexpr int kQ4Threads = 384;
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
 
+// Attention over records for longer query blocks: 128-row tiles on tcgen05,
+// keys split over CTAs (chunk_q4.cu).
+struct ChunkShape {
+  int D;              // 64 or 128
+  int qpt, rows;      // query positions and rows per tile (rows = qpt * g <= 128)
+  int m_tiles;        // ceil(seq_q / qpt)
+  int tiles;          // key tiles per group; with kv_lens, the most
+  int64_t groups;     // batch * heads_kv * m_tiles
+  int64_t places;     // groups * (tiles + kQ4Lead)
+  int grid, stages, smem_bytes;
+  bool fits;          // the kernel takes the problem
+  int64_t info_offset, part_ml_offset, part_o_offset, workspace_end;
+};
+struct ChunkArgs {
+  int qpt, rows, m_tiles, tiles, lead, places, stages, grid;
+  int2* info;         // per group: the opening CTA's partial slot, partials
+  float2* part_ml;    // [slot][row]
+  float* part_o;      // [slot][row][D]
+};
+constexpr int kChunkThreads = 512;
+ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count);
+int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs& a, uint8_t* ws,
+                    const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                    cudaStream_t stream);
+// Tensor map of Q tiles: boxes of qpt positions of the g heads of a kv head (api.cu).
+int encode_q_map(CUtensorMap* map, const void* q, const gqa_problem& p, int qpt);
+
 // ------------------------------------------------------------ fill: zeros (seq_k == 0) or NaN
 int launch_zero(const gqa_problem& p, void* out, cudaStream_t stream, bool nan);
 

@@ -122,6 +122,8 @@ extern "C" {
 #define GQA_KERNEL_Q4_PREFILL 7 /* gqa_forward_q4, long query blocks: the records are read back
                                    into 16-bit scratch, a part of the heads at a time, and
                                    attended to as by GQA_KERNEL_PREFILL */
+#define GQA_KERNEL_Q4_CHUNK 8 /* gqa_forward_q4, longer query blocks: 128-row tiles that unpack the
+                                 records once for all rows */
 
 /* One attention problem.  Strides are in elements. */
 typedef struct gqa_problem {
@@ -375,10 +377,11 @@ GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const v
  * paged caches, empty problems, rows without a visible key, the workspace and
  * the errors are those of gqa_forward.
  * Short query blocks (GQA_KERNEL_Q4) multiply the 4-bit codes themselves and
- * round neither keys nor values; long ones (GQA_KERNEL_Q4_PREFILL) round each
- * key and value once to the 16-bit type, in scratch that is part of
- * plan.workspace_bytes (at most 1 GiB unless one head's keys alone need more).
- * What decides is the estimated time of either way.
+ * round neither keys nor values; longer ones round each key and value once to
+ * the 16-bit type, on the way to the tensor cores (GQA_KERNEL_Q4_CHUNK) or in
+ * scratch (GQA_KERNEL_Q4_PREFILL; part of plan.workspace_bytes, at most 1 GiB
+ * unless one head's keys alone need more).  What decides is the estimated time
+ * of each.
  */
 GQA_API int gqa_query_q4(const gqa_problem* p, int sm_count, gqa_plan* plan);
 GQA_API int gqa_forward_q4(const gqa_problem* p, const void* q, const void* cache_k,
