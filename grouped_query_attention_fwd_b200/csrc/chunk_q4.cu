@@ -11,7 +11,8 @@
 //
 //   records --TMA--> raw ring --8 warps--> K, V in 16 bits, 128-byte swizzle
 //   S = Q K^T    tcgen05.mma, both from shared memory, S double-buffered in TMEM
-//   P = 2^(S - m)  4 warps, one thread per row; P over the first half of S
+//   P = 2^(S - m)  8 warps, two threads per row with half of the keys each,
+//                  which trade their maxima; P over the first half of S
 //   O += P V     tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
 //
 // Unpacking: a pair of codes becomes 128 + c (bf16) or 1024 + c (fp16) by one
@@ -25,11 +26,13 @@
 // scheduler on unpacking 32768 codes and 770 on 128 rows' softmax; the two
 // products need about 1000 of the tensor core.
 //
-// Warp roles (512 threads, one CTA per SM):
-//   warps 0-3   softmax and epilogue (thread t: row t)
-//   warps 4-11  unpacking (thread: one key, half of the dims)
-//   warp 12     TMA producer of Q tiles and records
-//   warp 13     TMEM allocator and MMA issuer (warps 14, 15 idle)
+// Warp roles (640 threads, one CTA per SM):
+//   warps 0-3   softmax of keys 0-63 of each tile, epilogue of half of O's
+//               columns (thread t: row t)
+//   warps 4-7   the same for keys 64-127 and the other half
+//   warps 8-15  unpacking (thread: one key, half of the dims)
+//   warp 16     TMA producer of Q tiles and records
+//   warp 17     TMEM allocator and MMA issuer (warps 18, 19 idle)
 // Every wait is bounded; a thread that gives up sets the abort flag and the
 // error word, and every role leaves its loops.
 #include <cuda_runtime.h>
@@ -47,14 +50,17 @@ namespace {
 using namespace prefill;
 using namespace q4;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = kChunkThreads;
+constexpr int kSoftmaxWarps = 8;
 constexpr int kConvWarps = 8;
-constexpr int kWarpLoad = 12;
-constexpr int kWarpMMA = 13;
-// Registers of the four warpgroups (setmaxnreg): softmax, unpacking twice, the
-// rest; together the launch's 128 a thread.
-constexpr int kSoftmaxRegs = 208, kConvRegs = 104, kIoRegs = 96;
-static_assert(kSoftmaxRegs + 2 * kConvRegs + kIoRegs <= 4 * 128, "register split");
+constexpr int kWarpLoad = 16;
+constexpr int kWarpMMA = 17;
+constexpr int HK = BN / 2;  // keys of a tile per softmax thread
+// Registers of the five warpgroups (setmaxnreg): softmax twice, unpacking
+// twice, the rest; together no more than the launch's 96 a thread.
+constexpr int kLaunchRegs = 96;
+constexpr int kSoftmaxRegs = 136, kConvRegs = 72, kIoRegs = 64;
+static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIoRegs <= 5 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // S buffers at 0 and 128
 
@@ -70,7 +76,7 @@ struct ChunkLayout {
   static constexpr int kVOff = kKOff + 2 * kTile;
   static constexpr int kRawOff = kVOff + 2 * kTile;
   static int bytes(int stages, int ragged_batch) {
-    return 1024 + kRawOff + stages * kRaw + (2 * stages + 20) * 8 + 32 +
+    return 1024 + kRawOff + stages * kRaw + (2 * stages + 20) * 8 + 32 + 2 * 2 * 128 * 4 +
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
 };
@@ -133,14 +139,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + 2;
   uint64_t* s_full = v_empty + 2;    // [J & 1] QK(J) done
-  uint64_t* p_full = s_full + 2;     // [J & 1] P(J) written (4 warps)
+  uint64_t* p_full = s_full + 2;     // [J & 1] P(J) written (8 warps)
   uint64_t* o_ready = p_full + 2;    // [J & 1] PV(J) done
   uint64_t* o_final = o_ready + 2;   // the share's last PV done
-  uint64_t* o_free = o_final + 1;    // O read by the epilogue (4 warps)
+  uint64_t* o_free = o_final + 1;    // O read by the epilogue (8 warps)
   uint64_t* mma_done = o_free + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int* len_s = reinterpret_cast<int*>(tmem_slot + 4);
+  float* xch = reinterpret_cast<float*>(tmem_slot + 4);  // [2][half][row]: what a row's threads trade
+  int* len_s = reinterpret_cast<int*>(xch + 512);
   int* pre_s = len_s + a.B;
 
   const int warp = threadIdx.x >> 5;
@@ -161,11 +168,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[i], kConvWarps);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], kSoftmaxWarps);
       mbar_init(&o_ready[i], 1);
     }
     mbar_init(o_final, 1);
-    mbar_init(o_free, 4);
+    mbar_init(o_free, kSoftmaxWarps);
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIoRegs));
     if (warp == kWarpLoad) {
       // ------------------------------------------------------------ producer
@@ -417,14 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait_drain(mma_done, 0);
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // -------------------------------------------------------------- unpacking
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // A thread takes one key and half of the dims: NG / 2 groups.  Eight
     // consecutive keys in a quarter-warp: neither the records' 80-byte rows
     // nor the swizzled 16-byte stores conflict.
     constexpr int G2 = NG / 2;
-    const int ct = static_cast<int>(threadIdx.x) - 128;
+    const int ct = static_cast<int>(threadIdx.x) - 256;
     const int half = ct >> 7, key = ct & 127;
     uint8_t* const row_at = smem + (CH == 2 ? half * L::kChunkBytes : 0) + key * 128;
     const int word0 = CH == 2 ? 0 : half * 4;  // first 16-byte piece of the row's chunk
@@ -493,95 +500,129 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int row = static_cast<int>(threadIdx.x);
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_col = tmem + lane_base + kOCol;
+    constexpr int HD = D / 2;
+    const int h = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t o_col = tmem + lane_base + kOCol + h * HD;
     const int hh = row / ca.qpt, qi = row % ca.qpt;
-    const bool live = warp * 32 < ca.rows;  // a warp without rows only keeps step
+    const bool live = (warp & 3) * 32 < ca.rows;  // a warp without rows only keeps step
+    uint32_t X = 0;  // values traded so far
+    // Publish v, meet the row's other thread, return its value; `flag` becomes
+    // the AND over the two warps.
+    auto trade = [&](float v, bool& flag) {
+      float* slot = xch + (X & 1u) * 256;
+      slot[h * 128 + row] = v;
+      flag = bar_and(1 + (warp & 3), 64, flag);
+      const float other = slot[(h ^ 1) * 128 + row];
+      ++X;
+      return other;
+    };
     uint32_t J = 0, n_share = 0;
     bool first_share = true;
+    bool ok = true;  // nothing has failed; carried to the next trade, so that no
+                     // warp is left alone at its named barrier
     each_share([&](const Share& sh) {
       const int q = sh.sl.q0 + qi;
       const bool row_valid = row < ca.rows && q < a.Sq;
-      float m_ref = -INFINITY, l = 0.f;
+      // Keys [row_lo, row_hi) that this row sees, and key tiles [all_beg,
+      // all_end) that every row sees all of.
+      int row_lo = 0, row_hi = sh.pr.len, all_beg = 0, all_end = sh.pr.len / BN;
+      if (a.causal) {
+        const int64_t off = pair_off(a, sh.pr);
+        row_hi = static_cast<int>(imax64(0, imin64(row_hi, q + off + 1)));
+        all_end = static_cast<int>(imax64(0, imin64(sh.pr.len, sh.sl.q0 + off + 1)) / BN);
+        if (a.window > 0) {
+          row_lo = static_cast<int>(imin64(row_hi, imax64(0, q + off - a.window + 1)));
+          all_beg = static_cast<int>(
+              imin64(all_end, (imax64(0, sh.sl.q_last + off - a.window + 1) + BN - 1) / BN));
+        }
+      }
+      float m_ref = -INFINITY, l = 0.f;  // m_ref is the same in both threads of a row
       for (int nt = sh.nt_beg; nt < sh.nt_end; ++nt, ++J) {
         const uint32_t s_col = tmem + lane_base + (J & 1u) * BN;
         // (Warp-uniform: every TMEM access below is made by the whole warp.)
-        if (!__all_sync(0xffffffffu, mbar_wait_hot(&s_full[J & 1u], (J >> 1) & 1u, abort_flag,
-                                                   a.err, kErrPrefillWait)))
-          return false;
-        if (live) {
+        bool okt = __all_sync(0xffffffffu,
+                              ok && mbar_wait_hot(&s_full[J & 1u], (J >> 1) & 1u, abort_flag,
+                                                  a.err, kErrPrefillWait));
+        if (!live) {
+          if (!okt) return false;
+          if (lane == 0) mbar_arrive(&p_full[J & 1u]);
+          continue;
+        }
+        // Wholly visible tiles work on raw scores and fold the scale into one
+        // FMA per element; the others test each key.
+        const bool fast = nt >= all_beg && nt < all_end && a.scale_log2 >= 0.f;
+        uint32_t r[HK];
+        float mx = -INFINITY;
+        if (okt) {
           tc_fence_after();
-          uint32_t r[BN];
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
-            tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[c * 32]));
+          tmem_ld32(s_col + h * HK, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+          tmem_ld32(s_col + h * HK + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
           tmem_ld_wait();
-          // Wholly visible tiles work on raw scores and fold the scale into
-          // one FMA per element; the others test each key.
-          const int cls = tile_class(a, sh.pr, sh.sl, nt, 0, 0);
-          const bool fast = cls == 2 && a.scale_log2 >= 0.f;
           if (!fast) {
-            uint32_t vb[4];
-            visible_bits<4>(vb, nullptr, nt * BN, a, sh.pr, q, false);
+            const int lo = row_lo - nt * BN - h * HK, hi = row_hi - nt * BN - h * HK;
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              r[c] = __float_as_uint(((vb[c >> 5] >> (c & 31)) & 1u)
-                                         ? __uint_as_float(r[c]) * a.scale_log2
-                                         : -INFINITY);
+            for (int c = 0; c < HK; ++c)
+              r[c] = __float_as_uint(c >= lo && c < hi ? __uint_as_float(r[c]) * a.scale_log2
+                                                       : -INFINITY);
           }
-          float part[8];
+          float part[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) part[e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) part[e] = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < BN; c += 16)
+          for (int c = 0; c < HK; c += 8)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              part[e] = fmax3(part[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + 8 + e]));
-          float mx = fmax3(fmax3(part[0], part[1], part[2]), fmax3(part[3], part[4], part[5]),
-                           fmaxf(part[6], part[7]));
+            for (int e = 0; e < 4; ++e)
+              part[e] = fmax3(part[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + 4 + e]));
+          mx = fmax3(part[0], part[1], fmaxf(part[2], part[3]));
           if (fast) mx *= a.scale_log2;
-          const float m_new = fmaxf(m_ref, mx);
-          const bool grow = m_new > m_ref + kRescaleLog2;  // also for -inf -> finite
-          const float alpha = grow ? fast_exp2(m_ref - m_new) : 1.f;
-          const bool o_live = grow && nt > sh.nt_beg && m_ref != -INFINITY;
-          if (grow) {
-            l *= alpha;
-            m_ref = m_new;
+        }
+        // Once traded, both halves of S are in registers: P may overwrite them.
+        tc_fence_before();
+        const float mx_other = trade(mx, okt);
+        tc_fence_after();
+        if (!okt) return false;
+        const float m_new = fmaxf(m_ref, fmaxf(mx, mx_other));
+        const bool grow = m_new > m_ref + kRescaleLog2;  // also for -inf -> finite
+        const float alpha = grow ? fast_exp2(m_ref - m_new) : 1.f;
+        const bool o_live = grow && nt > sh.nt_beg && m_ref != -INFINITY;
+        if (grow) {
+          l *= alpha;
+          m_ref = m_new;
+        }
+        const float ref = exp_ref(m_ref);
+        const float sc = fast ? a.scale_log2 : 1.f;
+        const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(-ref, -ref);
+        uint64_t lp[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) lp[e] = 0;
+#pragma unroll
+        for (int c = 0; c < HK / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c0 = c * 32 + 2 * e;
+            const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[c0]), __uint_as_float(r[c0 + 1])),
+                                      sc2, nref2);
+            const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
+            lp[e & 3] = f2_add(lp[e & 3], f2_pack(p0, p1));
+            pk[e] = pack_p<F16>(p0, p1);
           }
-          const float ref = exp_ref(m_ref);
-          const float sc = fast ? a.scale_log2 : 1.f;
-          const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(-ref, -ref);
-          uint64_t lp[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) lp[e] = 0;
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c0 = c * 32 + 2 * e;
-              const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[c0]), __uint_as_float(r[c0 + 1])),
-                                        sc2, nref2);
-              const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
-              lp[e & 3] = f2_add(lp[e & 3], f2_pack(p0, p1));
-              pk[e] = pack_p<F16>(p0, p1);
-            }
-            tmem_st16(s_col + c * 16, pk);
-          }
-          l += ((f2_lo(lp[0]) + f2_hi(lp[0])) + (f2_lo(lp[1]) + f2_hi(lp[1]))) +
-               ((f2_lo(lp[2]) + f2_hi(lp[2])) + (f2_lo(lp[3]) + f2_hi(lp[3])));
-          if (__any_sync(0xffffffffu, o_live)) {
-            // O holds the earlier tiles' P V with the old reference: rescale it
-            // once the previous tile's PV has completed.
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait_hot(&o_ready[(J - 1) & 1u], ((J - 1) >> 1) & 1u, abort_flag,
-                                          a.err, kErrPrefillWait)))
-              return false;
+          tmem_st16(s_col + h * (HK / 2) + c * 16, pk);
+        }
+        l += ((f2_lo(lp[0]) + f2_hi(lp[0])) + (f2_lo(lp[1]) + f2_hi(lp[1]))) +
+             ((f2_lo(lp[2]) + f2_hi(lp[2])) + (f2_lo(lp[3]) + f2_hi(lp[3])));
+        if (__any_sync(0xffffffffu, o_live)) {
+          // O holds the earlier tiles' P V with the old reference: rescale this
+          // half of it once the previous tile's PV has completed.
+          if (__all_sync(0xffffffffu,
+                         mbar_wait_hot(&o_ready[(J - 1) & 1u], ((J - 1) >> 1) & 1u, abort_flag,
+                                       a.err, kErrPrefillWait))) {
             tc_fence_after();
             const float f = o_live ? alpha : 1.f;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < HD / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(o_col + c * 32, o);
               tmem_ld_wait();
@@ -590,69 +631,74 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(o_col + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
               tmem_st16(o_col + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
             }
+          } else {
+            ok = false;
           }
-          tmem_st_wait();
-          tc_fence_before();
         }
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[J & 1u]);
       }
       // Epilogue: out, or this CTA's partial of a split group.
       const bool some = sh.nt_end > sh.nt_beg;
       const bool split = sh.c_lo != sh.c_hi;
-      if (some && !__all_sync(0xffffffffu, mbar_wait_hot(o_final, n_share & 1u, abort_flag, a.err,
-                                                         kErrPrefillWait)))
-        return false;
-      uint32_t r[D];
+      bool oke = __all_sync(0xffffffffu, ok && (!some || mbar_wait_hot(o_final, n_share & 1u,
+                                                                       abort_flag, a.err,
+                                                                       kErrPrefillWait)));
+      float l_other = 0.f;
+      if (live) l_other = trade(l, oke);
+      if (!oke) return false;
+      uint32_t r[HD];
       if (some && live) {
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+        for (int c = 0; c < HD / 32; ++c)
           tmem_ld32(o_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[c * 32]));
         tmem_ld_wait();
         tc_fence_before();
       } else {
 #pragma unroll
-        for (int e = 0; e < D; ++e) r[e] = 0u;
+        for (int e = 0; e < HD; ++e) r[e] = 0u;
       }
       if (some) {
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
         ++n_share;
       }
+      const int slot = cta * 2 + (first_share ? 0 : 1);
+      first_share = false;
+      if (threadIdx.x == 0 && (!split || sh.opens))
+        ca.info[sh.id] = split ? make_int2(slot, sh.c_hi - sh.c_lo + 1) : make_int2(0, 1);
+      if (!row_valid) return true;
       // O's columns are the dims with each eight as V's nibbles fell.
       constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // column of dim e of eight
-      const int slot = cta * 2 + (first_share ? 0 : 1);
-      if (split && sh.opens && threadIdx.x == 0)
-        ca.info[sh.id] = make_int2(slot, sh.c_hi - sh.c_lo + 1);
-      if (!split && threadIdx.x == 0) ca.info[sh.id] = make_int2(0, 1);
-      first_share = false;
-      if (row_valid) {
-        if (split) {
-          const int64_t at = static_cast<int64_t>(slot) * BM + row;
-          ca.part_ml[at] = make_float2(m_ref, l);
-          float* po = ca.part_o + at * D;
+      const float lsum = l + l_other;
+      if (split) {
+        const int64_t at = static_cast<int64_t>(slot) * BM + row;
+        if (h == 0) ca.part_ml[at] = make_float2(m_ref, lsum);
+        float* po = ca.part_o + at * D + h * HD;
 #pragma unroll
-          for (int d = 0; d < D; d += 4)
-            *reinterpret_cast<float4*>(po + d) = make_float4(
-                __uint_as_float(r[(d & ~7) + kAt[d & 7]]), __uint_as_float(r[(d & ~7) + kAt[(d & 7) + 1]]),
-                __uint_as_float(r[(d & ~7) + kAt[(d & 7) + 2]]),
-                __uint_as_float(r[(d & ~7) + kAt[(d & 7) + 3]]));
-        } else {
-          uint16_t* orow = a.out + sh.pr.b * a.os[0] +
-                           static_cast<int64_t>(sh.pr.kv * a.g + hh) * a.os[1] +
-                           static_cast<int64_t>(q) * a.os[2];
-          const float inv = 1.f / l;  // no visible key: 0 * inf = NaN
+        for (int d = 0; d < HD; d += 8)
 #pragma unroll
-          for (int d = 0; d < D; d += 8) {
-            if (d >= a.Dv) break;
-            uint32_t w[4];
+          for (int e = 0; e < 8; e += 4)
+            *reinterpret_cast<float4*>(po + d + e) =
+                make_float4(__uint_as_float(r[d + kAt[e]]), __uint_as_float(r[d + kAt[e + 1]]),
+                            __uint_as_float(r[d + kAt[e + 2]]), __uint_as_float(r[d + kAt[e + 3]]));
+      } else {
+        uint16_t* orow = a.out + sh.pr.b * a.os[0] +
+                         static_cast<int64_t>(sh.pr.kv * a.g + hh) * a.os[1] +
+                         static_cast<int64_t>(q) * a.os[2] + h * HD;
+        const float inv = 1.f / lsum;  // no visible key: 0 * inf = NaN
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<F16>(__uint_as_float(r[d + kAt[2 * e]]) * inv,
-                                __uint_as_float(r[d + kAt[2 * e + 1]]) * inv);
-            *reinterpret_cast<uint4*>(orow + d) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int d = 0; d < HD; d += 8) {
+          if (h * HD + d >= a.Dv) break;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack2<F16>(__uint_as_float(r[d + kAt[2 * e]]) * inv,
+                              __uint_as_float(r[d + kAt[2 * e + 1]]) * inv);
+          *reinterpret_cast<uint4*>(orow + d) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       return true;
@@ -729,7 +775,7 @@ int launch_t(const ChunkShape& s, const PrefillArgs& a, const ChunkArgs& ca, con
   }
   // The register split assumes the launch allocation it was sized for.
   cudaFuncAttributes fa{};
-  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != 128) {
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != kLaunchRegs) {
     cudaGetLastError();
     return GQA_ERR_CUDA;
   }

@@ -296,7 +296,7 @@ struct ChunkArgs {
   float2* part_ml;    // [slot][row]
   float* part_o;      // [slot][row][D]
 };
-constexpr int kChunkThreads = 512;
+constexpr int kChunkThreads = 640;
 ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count);
 int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs& a, uint8_t* ws,
                     const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
