@@ -81,6 +81,24 @@ struct ChunkLayout {
   }
 };
 
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t sub2(uint32_t x, uint32_t y, bool f16) {
   uint32_t r;
   if (f16)
@@ -433,8 +451,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int G2 = NG / 2;
     const int ct = static_cast<int>(threadIdx.x) - 256;
     const int half = ct >> 7, key = ct & 127;
-    uint8_t* const row_at = smem + (CH == 2 ? half * L::kChunkBytes : 0) + key * 128;
-    const int word0 = CH == 2 ? 0 : half * 4;  // first 16-byte piece of the row's chunk
+    // The row's 16-byte pieces in the swizzled tile: piece p at row_at ^ 16 p.
+    const uint32_t row_at = smem_u32(smem) + (CH == 2 ? half * L::kChunkBytes : half * 64) +
+                            key * 128;
+    const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
+    const uint32_t raw_at = smem_u32(smem) + L::kRawOff + key * P + half * G2 * 4;
+    const uint32_t code_at = smem_u32(smem) + L::kRawOff + key * P + kHeadBytes + half * G2 * 16;
     uint32_t J = 0;
     int s = 0;
     uint32_t parity = 0;
@@ -445,16 +467,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     each_share([&](const Share& sh) {
       for (int nt = sh.nt_beg; nt < sh.nt_end; ++nt, ++J) {
         if (!wait(&raw_full[s], parity)) return false;
-        const uint8_t* raw = smem + L::kRawOff + s * L::kRaw + key * P;
+        const bool held = nt * BN + key < sh.pr.len;
         uint32_t par[2][G2];
         uint4 code[2][G2];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int i = 0; i < G2; ++i) {
-            par[x][i] = *reinterpret_cast<const uint32_t*>(raw + x * BN * P + (half * G2 + i) * 4);
-            code[x][i] = *reinterpret_cast<const uint4*>(raw + x * BN * P + kHeadBytes +
-                                                         (half * G2 + i) * 16);
+            par[x][i] = ld_shared(raw_at + s * L::kRaw + x * BN * P + i * 4);
+            code[x][i] = ld_shared4(code_at + s * L::kRaw + x * BN * P + i * 16);
+            if (!held) par[x][i] = 0u;  // past the length: zeros
           }
         __syncwarp();
         if (lane == 0) mbar_arrive(&raw_empty[s]);
@@ -463,12 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           parity ^= 1u;
         }
         const uint32_t buf = J & 1u;
-        const bool held = nt * BN + key < sh.pr.len;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {  // K, then V
           uint64_t* const empty = x == 0 ? &k_empty[buf] : &v_empty[buf];
           if (J >= 2 && !wait(empty, ((J >> 1) - 1) & 1u)) return false;
-          uint8_t* const to = row_at + (x == 0 ? L::kKOff : L::kVOff) + buf * L::kTile;
+          const uint32_t to = row_at + (x == 0 ? L::kKOff : L::kVOff) + buf * L::kTile;
 #pragma unroll
           for (int i = 0; i < G2; ++i) {
             const uint32_t scale2 = __byte_perm(par[x][i], 0u, 0x1010);
@@ -484,10 +505,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 out.y = __byte_perm(v[2], v[3], 0x5410);
                 out.z = __byte_perm(v[0], v[1], 0x7632);
                 out.w = __byte_perm(v[2], v[3], 0x7632);
-              } else {       // as the nibbles fall; nothing past the length
-                out = held ? make_uint4(v[0], v[1], v[2], v[3]) : make_uint4(0u, 0u, 0u, 0u);
+              } else {       // as the nibbles fall
+                out = make_uint4(v[0], v[1], v[2], v[3]);
               }
-              *reinterpret_cast<uint4*>(to + (((word0 + i * 4 + j) ^ (key & 7)) << 4)) = out;
+              // (half * 64 is a multiple of 64 and swz of 16: the XOR of the
+              // piece's number stays inside the row's 128 bytes.)
+              st_shared4((to + (i * 4 + j) * 16) ^ swz, out);
             }
           }
           fence_proxy_async_smem();
@@ -607,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       sc2, nref2);
             const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
             lp[e & 3] = f2_add(lp[e & 3], f2_pack(p0, p1));
-            pk[e] = pack_p<F16>(p0, p1);
+            pk[e] = pack2<F16>(p0, p1);
           }
           tmem_st16(s_col + h * (HK / 2) + c * 16, pk);
         }
