@@ -10,7 +10,8 @@
 // second launch merges.
 //
 //   records --TMA--> raw ring --8 warps--> K, V in 16 bits, 128-byte swizzle
-//   S = Q K^T    tcgen05.mma, both from shared memory, S double-buffered in TMEM
+//   S = Q K^T    tcgen05.mma, Q from TMEM (copied in once per group), K from
+//                shared memory, S double-buffered in TMEM
 //   P = 2^(S - m)  8 warps, two threads per row with half of the keys each,
 //                  which trade their maxima; P over the first half of S
 //   O += P V     tcgen05.mma, P from TMEM, V from shared memory, O in TMEM
@@ -62,7 +63,7 @@ constexpr int kLaunchRegs = 96;
 constexpr int kSoftmaxRegs = 136, kConvRegs = 72, kIoRegs = 64;
 static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIoRegs <= 5 * kLaunchRegs, "register split");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOCol = 256;  // S buffers at 0 and 128
+constexpr uint32_t kOCol = 256, kQCol = 384;  // S buffers at 0 and 128
 
 template <int D>
 struct ChunkLayout {
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::kRawOff + R * L::kRaw);
   uint64_t* raw_empty = raw_full + R;
   uint64_t* q_full = raw_empty + R;
-  uint64_t* q_empty = q_full + 1;    // the share's last QK done
+  uint64_t* q_empty = q_full + 1;    // Q copied into TMEM
   uint64_t* k_full = q_empty + 1;    // [J & 1] K unpacked (8 warps)
   uint64_t* k_empty = k_full + 2;    // [J & 1] QK(J) done
   uint64_t* v_full = k_empty + 2;
@@ -378,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // execute in issue order, so QK(j + 2) may overwrite P(j) after PV(j).
       constexpr uint32_t idesc_qk = F16 ? idesc_f16_f32(BM, BN, 0, 0) : idesc_bf16_f32(BM, BN, 0, 0);
       constexpr uint32_t idesc_pv = F16 ? idesc_f16_f32(BM, D, 0, 1) : idesc_bf16_f32(BM, D, 0, 1);
-      const uint64_t dq = kmajor_desc(smem_u32(smem));
       const uint64_t dk0 = kmajor_desc(smem_u32(smem + L::kKOff));
       const uint64_t dv0 = mnmajor_desc(smem_u32(smem + L::kVOff), L::kChunkBytes);
       uint32_t Jq = 0, Jp = 0;  // tiles whose QK / PV have been issued
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __all_sync(0xffffffffu, mbar_wait_hot(bar, par, abort_flag, a.err,
                                                      kErrPrefillWait)) != 0;
       };
-      auto issue_qk = [&](bool last) {
+      auto issue_qk = [&]() {
         const uint32_t s = Jq & 1u;
         if (!wait(&k_full[s], (Jq >> 1) & 1u)) return false;
         tc_fence_after();
@@ -396,11 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t step = ((ks >> 2) * L::kChunkBytes + (ks & 3) * 32) >> 4;
-            tc_mma_ss(tmem + s * BN, dq + step, dk + step, idesc_qk, ks > 0 ? 1u : 0u);
+            tc_mma_ts(tmem + s * BN, tmem + kQCol + ks * 8, dk + step, idesc_qk, ks > 0 ? 1u : 0u);
           }
           tc_commit(&s_full[s]);
           tc_commit(&k_empty[s]);
-          if (last) tc_commit(q_empty);
         }
         __syncwarp();
         ++Jq;
@@ -428,12 +427,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       each_share([&](const Share& sh) {
         const int n = sh.nt_end - sh.nt_beg;
         if (n == 0) return true;
+        // Q into TMEM; the copy follows the last share's QKs on the tensor core.
         if (!wait(q_full, n_share & 1u)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            tc_cp_128x256b(tmem + kQCol + ks * 8,
+                           kmajor_desc(smem_u32(smem) + (ks >> 2) * L::kChunkBytes + (ks & 3) * 32));
+          tc_commit(q_empty);
+        }
+        __syncwarp();
         for (int i = 0; i < 2 && i < n; ++i)
-          if (!issue_qk(i == n - 1)) return false;
+          if (!issue_qk()) return false;
         for (int i = 0; i < n; ++i) {
           if (!issue_pv(i == 0, i == n - 1)) return false;
-          if (i + 2 < n && !issue_qk(i + 2 == n - 1)) return false;
+          if (i + 2 < n && !issue_qk()) return false;
         }
         ++n_share;
         return true;
