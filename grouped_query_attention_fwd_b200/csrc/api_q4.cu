@@ -19,7 +19,7 @@ constexpr int64_t kLim = int64_t(1) << 31;
 constexpr double kDecodeNs = 10000;
 constexpr double kSliceNs = 12000, kTwoTileNs = 2200, kReadBytesPerNs = 4500;
 // Launches and ends of the 128-row kernel, and a key tile of one of its SMs.
-constexpr double kChunkNs = 14000, kChunkTileNs = 1000;
+constexpr double kChunkNs = 20000;
 
 bool aligned(const void* ptr, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
@@ -82,6 +82,12 @@ gqa_problem slice_problem(const gqa_problem& p, int64_t b0, int64_t nb, int64_t 
 constexpr int64_t kSliceL2 = int64_t(64) << 20;     // scratch that stays in L2 beside the rest
 constexpr int64_t kSliceMost = int64_t(1) << 30;    // scratch of a slice, unless one head needs more
 
+// The most keys of an entry that its queries can see.
+int64_t keys_read(const gqa_problem& p) {
+  const int64_t w = p.window > 0 ? p.seq_q + p.window : p.seq_k;
+  return w < p.seq_k ? w : p.seq_k;
+}
+
 SlicePlan plan_slices(const gqa_problem& p, int sms) {
   SlicePlan s{};
   const int64_t g = p.heads_q / p.heads_kv;
@@ -112,21 +118,24 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
   s.launches = static_cast<int>(s.slices) *
                (2 + (p.has_mask ? 1 : 0) + (f.order_offset >= 0 ? 1 : 0));
   const double rounds = double((s.nb * s.nh * items + sms - 1) / sms);
+  const int64_t keys = keys_read(p);
   const double bytes = 2.0 * double(p.batch * p.heads_kv) *
-                       double(p.seq_k * (q4::record_bytes(static_cast<int>(p.head_dim)) +
+                       double(keys * (q4::record_bytes(static_cast<int>(p.head_dim)) +
                                          2 * p.head_dim));
-  s.ns = double(s.slices) * (kSliceNs + rounds * double((p.seq_k + 127) / 128) * kTwoTileNs) +
+  s.ns = double(s.slices) * (kSliceNs + rounds * double((keys + 127) / 128) * kTwoTileNs) +
          bytes / kReadBytesPerNs;
   return s;
 }
 
 // Estimated times of the other two ways over the same problem.
-double decode_ns(const DecodeShape& s, int sms) {
-  return kDecodeNs + double(s.units) / sms * kQ4UnitNs;
+double decode_ns(const gqa_problem& p, const DecodeShape& s, int sms) {
+  const double units = double(s.groups) * double((keys_read(p) + 127) / 128);
+  return kDecodeNs + units / sms * kQ4UnitNs;
 }
 
-double chunk_ns(const ChunkShape& s, int sms) {
-  return kChunkNs + double(s.places) / sms * kChunkTileNs;
+double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
+  const double places = double(s.groups) * double((keys_read(p) + 127) / 128 + kQ4Lead);
+  return kChunkNs + places / sms * (s.nq == 2 ? kChunkPairNs : kChunkTileNs);
 }
 
 // The way to attend: a pass over the records per 8 rows of a kv head (one pass
@@ -135,10 +144,10 @@ double chunk_ns(const ChunkShape& s, int sms) {
 int pick_way(const gqa_problem& p, const DecodeShape& d, const ChunkShape& c, const SlicePlan& s,
              int sms) {
   if (d.passes <= 1 || p.seq_q <= 1) return GQA_KERNEL_Q4;
-  double best = decode_ns(d, sms);
+  double best = decode_ns(p, d, sms);
   int way = GQA_KERNEL_Q4;
-  if (c.fits && chunk_ns(c, sms) < best) {
-    best = chunk_ns(c, sms);
+  if (c.fits && chunk_ns(p, c, sms) < best) {
+    best = chunk_ns(p, c, sms);
     way = GQA_KERNEL_Q4_CHUNK;
   }
   return s.ns < best ? GQA_KERNEL_Q4_PREFILL : way;
@@ -234,7 +243,10 @@ int run_slices(const gqa_problem& p, const SlicePlan& s, int sms, const void* q,
         a.num_pages = p.num_pages;
       }
       a.vec = true;
-      a.leave_tail = true;  // the prefill never uses what lies past a length
+      // The prefill uses nothing past a length, nor key tiles below the window
+      // of the first query.
+      a.leave_tail = true;
+      a.from = p.window > 0 ? p.causal_offset - p.seq_k - p.window + 1 : -kLim;
       int rc = launch_q4_read(a, f16, stream);
       if (rc != GQA_OK) return rc;
       rc = launch_prefill_call(

@@ -261,6 +261,8 @@ struct Q4RowsArgs {
   int64_t bt_stride, page_size, num_pages;
   bool vec;                 // every 16-bit row starts on 16 bytes
   bool leave_tail;          // read: rows past the length are left as they are, not zeroed
+  int64_t from;           // with leave_tail: rows below len + from (down to a whole 128-key
+                          // tile) are not written either
 };
 int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
@@ -283,20 +285,23 @@ struct ChunkShape {
   int D;              // 64 or 128
   int qpt, rows;      // query positions and rows per tile (rows = qpt * g <= 128)
   int m_tiles;        // ceil(seq_q / qpt)
+  int nq, m_groups;   // query tiles per group (1 or 2); ceil(m_tiles / nq)
   int tiles;          // key tiles per group; with kv_lens, the most
-  int64_t groups;     // batch * heads_kv * m_tiles
+  int64_t groups;     // batch * heads_kv * m_groups
   int64_t places;     // groups * (tiles + kQ4Lead)
   int grid, stages, smem_bytes;
   bool fits;          // the kernel takes the problem
   int64_t info_offset, part_ml_offset, part_o_offset, workspace_end;
 };
 struct ChunkArgs {
-  int qpt, rows, m_tiles, tiles, lead, places, stages, grid;
+  int qpt, rows, m_tiles, nq, m_groups, tiles, lead, places, stages, grid;
   int2* info;         // per group: the opening CTA's partial slot, partials
-  float2* part_ml;    // [slot][row]
-  float* part_o;      // [slot][row][D]
+  float2* part_ml;    // [slot][query tile][row]
+  float* part_o;      // [slot][query tile][row][D]
 };
 constexpr int kChunkThreads = 640;
+// Time of a key tile on an SM, with one query tile and with two.
+constexpr int kChunkTileNs = 1950, kChunkPairNs = 2600;
 ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count);
 int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs& a, uint8_t* ws,
                     const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,

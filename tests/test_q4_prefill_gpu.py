@@ -42,11 +42,13 @@ CASES = [
     # B, Hq, Hkv, Sq, Sk, D, dtype, lens, page, window, mask, kernel
     (4, 8, 2, 512, 2048, 128, "bf16", None, 0, 0, False, "q4_chunk"),
     (4, 8, 2, 512, 2048, 128, "fp16", [2048, 1, 513, 700], 64, 0, False, "q4_chunk"),
-    (3, 12, 2, 700, 1536, 64, "bf16", [1536, 900, 701], 128, 300, False, "q4_chunk"),
-    (2, 8, 1, 33, 5000, 96, "fp16", None, 0, 0, False, "q4_chunk"),
+    (3, 12, 2, 700, 1536, 64, "bf16", [1536, 900, 701], 128, 300, False, "q4_prefill"),
+    (2, 8, 1, 33, 20000, 96, "fp16", None, 0, 0, False, "q4_chunk"),
+    (3, 8, 2, 30, 20032, 128, "bf16", [20000, 30, 9000], 64, 0, False, "q4_chunk"),
+    (2, 4, 1, 31, 60000, 64, "fp16", None, 0, 50000, False, "q4_chunk"),
     (2, 16, 1, 9, 30000, 128, "bf16", [30000, 0], 0, 0, False, "q4_chunk"),
     (1, 5, 1, 300, 12345, 40, "bf16", None, 0, 9000, False, "q4_chunk"),
-    (5, 3, 3, 300, 1000, 120, "fp16", [1000, 300, 299, 129, 128], 0, 0, False, "q4_chunk"),
+    (5, 3, 3, 500, 1000, 120, "fp16", [1000, 300, 299, 129, 128], 0, 0, False, "q4_chunk"),
     (12, 8, 2, 1024, 8192, 128, "bf16", None, 0, 0, False, "q4_chunk"),
     (4, 8, 4, 640, 1111, 80, "bf16", None, 0, 0, True, "q4_prefill"),
     (1, 32, 8, 2048, 2048, 128, "bf16", None, 0, 0, False, "q4_prefill"),
