@@ -96,14 +96,15 @@ struct ChunkLayout {
 
 __device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ uint4 ld_shared4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared4(uint32_t addr, const uint4& v) {
@@ -500,9 +501,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < G2; ++i) {
             par[i] = ld_shared(raw_at + s * L::kRaw + (half * G2 + i) * 4);
             code[i] = ld_shared4(raw_at + s * L::kRaw + kHeadBytes + (half * G2 + i) * 16);
-            if (!held) par[i] = 0u;  // past the length: zeros
           }
-          __syncwarp();
+          // The stage is handed back once its words have come: a load only
+          // issued may wait behind the products' operand reads until the next
+          // copy has landed (seen: results that changed from call to call).
+          // Branching on the words waits for them; the branch itself does nothing.
+          uint32_t any = 0u;
+#pragma unroll
+          for (int i = 0; i < G2; ++i)
+            any ^= par[i] ^ code[i].x ^ code[i].y ^ code[i].z ^ code[i].w;
+          if (__any_sync(0xffffffffu, any == 0xA5A5A5A5u)) __nanosleep(0);
+#pragma unroll
+          for (int i = 0; i < G2; ++i)
+            if (!held) par[i] = 0u;  // past the length: zeros
           if (lane == 0) mbar_arrive(&raw_empty[s]);
           if (++s == R) {
             s = 0;
@@ -700,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c_beg = nq == 1 ? X * (kCols / 2) : 0;
       const int c_end = nq == 1 ? c_beg + kCols / 2 : kCols;
       for (int c = c_beg; c < c_end; ++c) {
+        __syncwarp();  // (the TMEM loads below are the whole warp's)
         float o[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0.f * inv;

@@ -7,6 +7,8 @@ defines the record that a token's K or V row of one head becomes:
 
 Calls with arguments of sizes and strides already seen reuse the checked
 problem descriptor of the first such call; pointers are taken anew each time.
+Each call in a captured graph has a workspace of its own, which every replay
+clears: a caller who wants ``device_status`` after replays passes a workspace.
 """
 from __future__ import annotations
 

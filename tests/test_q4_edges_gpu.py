@@ -1,0 +1,218 @@
+"""The 4-bit cache where calls meet: threads, streams, captured steps, a shared
+workspace, offsets past 32 bits, and a wait that runs out.  Values are checked
+against eager calls on fresh workspaces, which other tests check against the
+oracle; equal launches give equal bits."""
+import threading
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gqa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    import grouped_query_attention_fwd_b200 as m
+    return m
+
+
+def _cache(gqa, B, Hkv, S, D, dtype=torch.bfloat16, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ck = torch.zeros(B, Hkv, S, gqa.q4_record_bytes(D), dtype=torch.uint8, device="cuda")
+    cv = torch.zeros_like(ck)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn(B, Hkv, S, D, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    gqa.kv_append_q4(ck, cv, k, v, lens)
+    return ck, cv
+
+
+def _q(B, Hq, Sq, D, dtype=torch.bfloat16, seed=1):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(B, Hq, Sq, D, generator=gen, device="cuda").to(dtype)
+
+
+# One call of each way of attending, over the same cache: (Sq, mask, kernel).
+WAYS = [(1, False, "q4"), (1, True, "q4"), (512, False, "q4_chunk"), (700, True, "q4_prefill")]
+
+
+def _ways(gqa, ck, cv):
+    B, Hkv, S, _ = ck.shape
+    calls = []
+    for i, (Sq, masked, kernel) in enumerate(WAYS):
+        q = _q(B, 4 * Hkv, Sq, 128, seed=10 + i)
+        kw = dict(causal=True, causal_offset="bottom_right")
+        if masked:
+            gen = torch.Generator(device="cuda").manual_seed(20 + i)
+            kw["mask"] = torch.rand(B, Sq, S, generator=gen, device="cuda") < 0.8
+        assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == kernel
+        calls.append((q, kw))
+    return calls
+
+
+def _fresh(gqa, q, ck, cv, kw):
+    n = gqa.query_q4(q, ck, cv, **kw)["workspace_bytes"]
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    out = gqa.forward_q4(q, ck, cv, workspace=ws, **kw)
+    assert gqa.device_status(ws) == gqa.GQA_OK
+    return out
+
+
+def test_ways_share_a_workspace(gqa):
+    ck, cv = _cache(gqa, 4, 2, 2048, 128)
+    calls = _ways(gqa, ck, cv)
+    want = [_fresh(gqa, q, ck, cv, kw) for q, kw in calls]
+    most = max(gqa.query_q4(q, ck, cv, **kw)["workspace_bytes"] for q, kw in calls)
+    ws = torch.zeros(most, dtype=torch.uint8, device="cuda")
+    for order in ([0, 2, 1, 3], [3, 0, 1, 2], [2, 3, 1, 0]):
+        got = [(i, gqa.forward_q4(calls[i][0], ck, cv, workspace=ws, **calls[i][1]))
+               for i in order]
+        assert gqa.device_status(ws) == gqa.GQA_OK
+        assert all(torch.equal(o, want[i]) for i, o in got)
+
+
+def test_threads_on_one_stream(gqa):
+    """Calls of several launches from two threads keep their scratch apart."""
+    ck, cv = _cache(gqa, 4, 2, 2048, 128)
+    calls = _ways(gqa, ck, cv)
+    want = [_fresh(gqa, q, ck, cv, kw) for q, kw in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(t):
+        for _ in range(25):
+            for i in ([2, 3, 1, 0], [3, 1, 2, 0])[t]:
+                q, kw = calls[i]
+                got[t].append((i, gqa.forward_q4(q, ck, cv, **kw)))
+
+    threads = [threading.Thread(target=work, args=(t,)) for t in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert gqa.device_status() == gqa.GQA_OK
+    assert len(got[0]) == len(got[1]) == 100
+    assert all(torch.equal(o, want[i]) for t in range(2) for i, o in got[t])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,S,D,dtype,kernel", [
+    (4, 8, 2, 512, 2048, 128, torch.bfloat16, "q4_chunk"),
+    (4, 8, 2, 512, 2048, 128, torch.float16, "q4_chunk"),
+    (4, 8, 2, 512, 2048, 64, torch.bfloat16, "q4_chunk"),
+    (8, 32, 8, 32, 8192, 128, torch.bfloat16, "q4_chunk"),
+    (8, 32, 8, 1, 8192, 128, torch.bfloat16, "q4"),
+    (8, 32, 8, 5, 4000, 64, torch.float16, "q4"),
+])
+def test_same_bits_call_after_call(gqa, B, Hq, Hkv, Sq, S, D, dtype, kernel):
+    """A tile refilled before its last reader is done would change some calls."""
+    ck, cv = _cache(gqa, B, Hkv, S, D, dtype)
+    q = _q(B, Hq, Sq, D, dtype)
+    kw = dict(causal=True, causal_offset="bottom_right")
+    assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == kernel
+    outs = [gqa.forward_q4(q, ck, cv, **kw) for _ in range(60)]
+    assert gqa.device_status() == gqa.GQA_OK
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_stream_argument(gqa):
+    ck, cv = _cache(gqa, 2, 2, 900, 96, torch.float16)
+    q = _q(2, 8, 3, 96, torch.float16)
+    kw = dict(causal=True, causal_offset="bottom_right")
+    want = gqa.forward_q4(q, ck, cv, **kw)
+    wk, wv = gqa.kv_read_q4(ck, cv, 96, torch.float16)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out = gqa.forward_q4(q, ck, cv, stream=s.cuda_stream, **kw)
+    k, v = gqa.kv_read_q4(ck, cv, 96, torch.float16, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(out, want) and torch.equal(k, wk) and torch.equal(v, wv)
+    # An append on the other stream, read on it too: the same records again.
+    c2 = [torch.zeros_like(ck), torch.zeros_like(cv)]
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    gqa.kv_append_q4(c2[0], c2[1], wk, wv, lens, stream=s.cuda_stream)
+    s.synchronize()
+    assert lens.tolist() == [900, 900]
+
+
+def test_captured_generation(gqa):
+    """A captured step that advances its lengths, replayed token after token."""
+    B, Hkv, D, cap, steps = 3, 2, 64, 300, 5
+    new = [torch.empty(B, Hkv, 1, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q = torch.empty(B, 8, 1, D, dtype=torch.bfloat16, device="cuda")
+    rows = [_q(B, Hkv, steps, D, seed=30 + i) for i in range(2)]
+    qs = _q(B, 8, steps, D, seed=40)
+    ck, cv = _cache(gqa, B, Hkv, cap, D)
+    start = torch.tensor([0, 64, cap - steps], dtype=torch.int32, device="cuda")
+    kw = dict(causal=True, causal_offset="bottom_right")
+
+    def step(c, lens, k, v, x):
+        gqa.kv_append_q4(c[0], c[1], k, v, lens)
+        return gqa.forward_q4(x, c[0], c[1], kv_lens=lens, **kw)
+
+    c1, l1 = (ck.clone(), cv.clone()), start.clone()
+    want = [step(c1, l1, rows[0][:, :, t:t + 1].contiguous(), rows[1][:, :, t:t + 1].contiguous(),
+                 qs[:, :, t:t + 1].contiguous()) for t in range(steps)]
+    torch.cuda.synchronize()
+    c2, l2 = (ck.clone(), cv.clone()), start.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(c2, l2, new[0], new[1], q)
+    for t in range(steps):
+        for dst, src in ((new[0], rows[0]), (new[1], rows[1]), (q, qs)):
+            dst.copy_(src[:, :, t:t + 1])
+        g.replay()
+        assert torch.equal(out, want[t])
+    assert torch.equal(l1, l2) and torch.equal(c1[0], c2[0]) and torch.equal(c1[1], c2[1])
+
+
+def test_offsets_past_32_bits(gqa):
+    """The last rows of a cache of 4.5 GB (x 2) are those of a small one."""
+    cap, n, D, tail = 56_000_000, 320, 128, 7
+    if torch.cuda.mem_get_info()[0] < 14 << 30:
+        pytest.skip("needs 14 GB")
+    R = gqa.q4_record_bytes(D)
+    assert (cap - n) * R > 1 << 32
+    big = [torch.empty(1, 1, cap, R, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    small = [torch.zeros(1, 1, n, R, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    k, v = _q(1, 1, n, D, seed=50), _q(1, 1, n, D, seed=51)
+    at, zero = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (cap - n - tail, 0))
+    for c in big:
+        c[:, :, -n - tail - 200:] = 0
+    gqa.kv_append_q4(big[0], big[1], k, v, at)
+    gqa.kv_append_q4(small[0], small[1], k, v, zero)
+    assert at.item() == cap - tail
+    for b, s in zip(big, small):
+        assert torch.equal(b[:, :, cap - n - tail:cap - tail], s)
+    got = gqa.kv_read_q4(big[0], big[1], D, torch.bfloat16, kv_lens=at, start=cap - n - tail, n=n)
+    want = gqa.kv_read_q4(small[0], small[1], D, torch.bfloat16)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for Sq in (1, 5, 40):
+        q = _q(1, 4, Sq, D, seed=52 + Sq)
+        kw = dict(causal=True, causal_offset="bottom_right", window=n - Sq)
+        a = gqa.forward_q4(q, big[0], big[1], kv_lens=at, **kw).double()
+        b = gqa.forward_q4(q, small[0], small[1], **kw).double()
+        # Two results of the same sums in other tiles: P's and the result's
+        # roundings differ, each at most half a step of 2^-8 and 2^-11.
+        assert float((a - b).norm() / b.norm()) <= 2 * (2.0 ** -8 + 2.0 ** -8)
+    assert gqa.device_status() == gqa.GQA_OK
+
+
+@pytest.mark.parametrize("unit", [0, 100, 383])
+def test_wait_runs_out_and_is_reported(gqa, unit):
+    """A launch whose producer withholds one tile's copies gives up its bounded
+    wait and says so; the next call with the same workspace is right."""
+    ck, cv = _cache(gqa, 4, 4, 3000, 128)
+    q = _q(4, 16, 1, 128)
+    plan = gqa.query_q4(q, ck, cv)
+    assert plan["kernel_name"] == "q4" and plan["work_units"] == 384
+    want = _fresh(gqa, q, ck, cv, {})
+    ws = torch.zeros(plan["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    gqa.debug_decode_withhold(unit, 200_000)  # 200 us limit, this launch only
+    gqa.forward_q4(q, ck, cv, workspace=ws)
+    assert gqa.device_status(ws) == gqa.GQA_ERR_TIMEOUT
+    out = gqa.forward_q4(q, ck, cv, workspace=ws)
+    assert gqa.device_status(ws) == gqa.GQA_OK
+    assert torch.equal(out, want)
