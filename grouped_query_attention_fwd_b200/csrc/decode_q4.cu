@@ -912,10 +912,6 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
             for (int t = 0; t < NG; t += 2)
               ldmatrix_x4_trans(vw[t][0], vw[t][1], vw[t + 1][0], vw[t + 1][1],
                                 vb + j * 16 * P + at + t * 16);
-            if (j == kSub - 1) {  // all of the chunk is in registers
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&empty[s]);
-            }
 #pragma unroll
             for (int y = 0; y < 4; ++y)
               sv[j][y] = fast_exp2(fmaf(sv[j][y], kWhole ? fac[y & 1] : 1.f, m_neg[y & 1]));
@@ -953,6 +949,10 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
               }
             }
           }
+          // Handed back when every word has been used: a load that has only
+          // been issued is no proof that it has come.
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[s]);
         };
         if (whole)
           rest(BoolConst<true>{});
