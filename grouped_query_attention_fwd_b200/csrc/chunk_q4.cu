@@ -35,11 +35,11 @@
 // Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 180 us,
 // 760 TFLOP/s; a 128-key tile costs an SM about 2.6 us with two query tiles and
 // 1.95 us with one, of which the products need 1.1 us and 0.55 us.  Bound: the
-// unpacking warps and the softmax, which share the issue slots (without the
-// unpacking's arithmetic and stores 164 us, without the softmax 154 us, without
-// both 145 us).  With four unpacking warps of twice the work each it took 197
-// us; a whole S row per thread costs some spills at 168 registers, fewer cost
-// more (152: 189 us, 136: 249 us).
+// unpacking warps and the softmax, which share the issue slots.  With four
+// unpacking warps of twice the work each it took 197 us (164 us without their
+// arithmetic and stores, 154 us without the softmax, 145 us without either).  A
+// whole S row per thread costs some spills at 168 registers; fewer cost more
+// (152: 189 us, 136: 249 us).
 //
 // Warp roles (640 threads, one CTA per SM):
 //   warps 0-3   softmax of X = 0 and its epilogue (thread t: row t)
