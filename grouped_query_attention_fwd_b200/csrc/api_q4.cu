@@ -58,7 +58,7 @@ struct SlicePlan {
   int64_t nb, nh;            // entries and kv heads per slice (nb > 1 only with every head)
   int64_t head_bytes;        // scratch of one kv head's K (or V)
   int64_t k_offset, v_offset, workspace_end;
-  int64_t slices;
+  int64_t slices, work;      // and the prefill's work items of all of them
   int launches;
   double ns;                 // estimated time
 };
@@ -109,14 +109,28 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
     s.nb = 1;
     s.nh = heads;
   }
-  const gqa_problem c = slice_problem(p, 0, s.nb, s.nh);
-  const PrefillShape f = plan_prefill(c, sms);
-  s.k_offset = (f.workspace_end + 255) / 256 * 256;
+  // Slices of up to four sizes (the last of the entries and of the heads may be
+  // narrower), each with a prefill plan of its own: a narrower one may need more
+  // scratch (the item order that a full one is too large to sort).  K and V
+  // start past all of them.
+  const int64_t nbs[2] = {p.batch / s.nb, p.batch % s.nb > 0 ? 1 : 0};
+  const int64_t nhs[2] = {p.heads_kv / s.nh, p.heads_kv % s.nh > 0 ? 1 : 0};
+  s.slices = (nbs[0] + nbs[1]) * (nhs[0] + nhs[1]);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t count = nbs[i & 1] * nhs[i >> 1];
+    if (count == 0) continue;
+    const PrefillShape f =
+        plan_prefill(slice_problem(p, 0, (i & 1) != 0 ? p.batch % s.nb : s.nb,
+                                   (i >> 1) != 0 ? p.heads_kv % s.nh : s.nh),
+                     sms);
+    if (f.workspace_end > s.k_offset) s.k_offset = f.workspace_end;
+    s.launches += static_cast<int>(count) *
+                  (2 + (p.has_mask ? 1 : 0) + (f.order_offset >= 0 ? 1 : 0));
+    s.work += count * f.work;
+  }
+  s.k_offset = (s.k_offset + 255) / 256 * 256;
   s.v_offset = s.k_offset + s.nb * s.nh * s.head_bytes;
   s.workspace_end = s.v_offset + s.nb * s.nh * s.head_bytes;
-  s.slices = (p.batch + s.nb - 1) / s.nb * ((p.heads_kv + s.nh - 1) / s.nh);
-  s.launches = static_cast<int>(s.slices) *
-               (2 + (p.has_mask ? 1 : 0) + (f.order_offset >= 0 ? 1 : 0));
   const double rounds = double((s.nb * s.nh * items + sms - 1) / sms);
   const int64_t keys = keys_read(p);
   const double bytes = 2.0 * double(p.batch * p.heads_kv) *
@@ -191,7 +205,7 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
     plan->block = kPrefillThreads;
     plan->smem_bytes = f.smem_bytes;
     plan->launches = sl.launches;
-    plan->work_units = static_cast<int32_t>(f.work * sl.slices);
+    plan->work_units = static_cast<int32_t>(sl.work);
     plan->workspace_bytes = (sl.workspace_end + 255) / 256 * 256;
     return GQA_OK;
   }

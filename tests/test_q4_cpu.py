@@ -208,3 +208,32 @@ def test_binding_refuses(gqa):
     with pytest.raises(ValueError):
         gqa.query_q4(x, c[..., :64], c[..., :64], sm_count=148)
     assert gqa.query_q4(x, c, c, sm_count=148)["kernel_name"] == "q4"
+
+
+@pytest.mark.parametrize("B,Hkv,g,Sq,Sk,D,entries,heads", [
+    # Widths of the slices (entries x heads); the prefill sorts its items by
+    # cost, which takes scratch, in the narrow ones only.
+    (1, 8, 8, 40000, 40000, 64, [1], [6, 2]),
+    (1, 8, 16, 43000, 43000, 128, [1], [3, 3, 2]),
+    (1, 4, 16, 40960, 40960, 128, [1], [3, 1]),
+    (1, 8, 16, 28672, 28672, 80, [1], [7, 1]),
+    (5, 1, 128, 2050, 65536, 64, [4, 1], [1]),
+    # And in all of them, or in none.
+    (2, 24, 4, 1024, 8192, 128, [1, 1], [16, 8]),
+    (1, 8, 16, 60000, 60000, 128, [1], [2, 2, 2, 2]),
+])
+def test_slices_of_every_width_keep_clear_of_the_keys(gqa, B, Hkv, g, Sq, Sk, D, entries, heads):
+    rc, plan = _rc(gqa, _problem(gqa, B, Hkv * g, Hkv, Sq, Sk, D, mask=True))
+    assert rc == 0 and gqa.KERNEL_NAMES[plan.kernel] == "q4_prefill"
+    head = -(-Sk * D * 2 // 256) * 256
+    keys_at = plan.workspace_bytes - 2 * entries[0] * heads[0] * head
+    launches = work = 0
+    for nb in entries:
+        for nh in heads:
+            part = gqa.query_problem(gqa.make_problem(
+                0, nb, nh * g, nh, Sq, Sk, D, *[(nh * g * Sq * D, Sq * D, D, 1)] * 4,
+                (Sq * Sk, Sk, 1)), 148)
+            assert part.workspace_bytes <= keys_at, (nb, nh)
+            launches += 1 + part.launches
+            work += part.work_units
+    assert plan.launches == launches and plan.work_units == work

@@ -174,3 +174,39 @@ def test_long_block_in_a_graph(gqa, Sq, masked):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_a_narrow_last_slice_keeps_its_keys(gqa):
+    """Five entries in slices of four and one, of which only the narrow one sorts
+    its items: its first keys, where a wrong place for the order would fall, are
+    all that every other query sees."""
+    B, g, Sq, Sk, D = 5, 128, 2050, 65536, 64
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB")
+    ck, k64 = _records(gqa, B, 1, Sk, D, "bf16", 11, True)
+    cv, v64 = _records(gqa, B, 1, Sk, D, "bf16", 12, False)
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    q = torch.randn(B, g, Sq, D, generator=gen, device="cuda").bfloat16()
+    mask = torch.zeros(B, Sq, Sk, dtype=torch.bool, device="cuda")
+    mask[:, ::2, :40] = True
+    mask[:, 1::2, 5::3] = True
+    plan = gqa.query_q4(q, ck, cv, mask=mask)
+    assert plan["kernel_name"] == "q4_prefill" and plan["launches"] == 7
+    out = gqa.forward_q4(q, ck, cv, mask=mask)
+    assert gqa.device_status() == gqa.GQA_OK
+    unit, scale = u.UNIT["bf16"], 1.0 / math.sqrt(D)
+    rows = [0, 1, 2, 255, 256, 1024, 1025, 2048, 2049]
+    for b in range(B):
+        k, v = k64[b, 0], v64[b, 0]
+        for i in rows:
+            qi = q[b, :, i].double()
+            s = (qi @ k.T * scale).masked_fill(~mask[b, i], -math.inf)
+            p = torch.softmax(s, -1)
+            ref = p @ v
+            # The roundings of test_long_query_blocks.
+            move = 2.1 * scale * unit * (qi.abs() @ k.abs().T).amax(-1, keepdim=True)
+            bound = (p @ v.abs()) * (2.02 * unit + move + 2.0 ** -14) + 1.01 * unit * ref.abs() + \
+                2.0 ** -24
+            err = (out[b, :, i].double() - ref).abs()
+            assert torch.all(err <= bound), (b, i, float((err / bound).max()))
+            assert float(err.norm() / ref.norm()) <= 1e-2, (b, i)
