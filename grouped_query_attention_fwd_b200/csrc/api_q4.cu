@@ -154,17 +154,21 @@ double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
 
 // The way to attend: a pass over the records per 8 rows of a kv head (one pass
 // where it has no more), 128-row tiles that unpack each record once, or the
-// two-tile prefill over 16-bit scratch.
-int pick_way(const gqa_problem& p, const DecodeShape& d, const ChunkShape& c, const SlicePlan& s,
-             int sms) {
+// two-tile prefill over 16-bit scratch.  The last two are planned, and their
+// plans filled in, only where the first is not taken outright: the tiles of a
+// single token of more than 128 query heads per kv head would hold no query
+// position.
+int pick_way(const gqa_problem& p, const DecodeShape& d, int sms, ChunkShape* c, SlicePlan* s) {
   if (d.passes <= 1 || p.seq_q <= 1) return GQA_KERNEL_Q4;
+  *c = plan_chunk_q4(p, sms);
+  *s = plan_slices(p, sms);
   double best = decode_ns(p, d, sms);
   int way = GQA_KERNEL_Q4;
-  if (c.fits && chunk_ns(p, c, sms) < best) {
-    best = chunk_ns(p, c, sms);
+  if (c->fits && chunk_ns(p, *c, sms) < best) {
+    best = chunk_ns(p, *c, sms);
     way = GQA_KERNEL_Q4_CHUNK;
   }
-  return s.ns < best ? GQA_KERNEL_Q4_PREFILL : way;
+  return s->ns < best ? GQA_KERNEL_Q4_PREFILL : way;
 }
 
 int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
@@ -187,9 +191,9 @@ int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {
     return GQA_OK;
   }
   const DecodeShape s = plan_decode_q4(p, sm_count);
-  const ChunkShape c = plan_chunk_q4(p, sm_count);
-  const SlicePlan sl = plan_slices(p, sm_count);
-  plan->kernel = pick_way(p, s, c, sl, sm_count);
+  ChunkShape c{};
+  SlicePlan sl{};
+  plan->kernel = pick_way(p, s, sm_count, &c, &sl);
   if (plan->kernel == GQA_KERNEL_Q4_CHUNK) {
     plan->grid = c.grid;
     plan->block = kChunkThreads;

@@ -237,3 +237,15 @@ def test_slices_of_every_width_keep_clear_of_the_keys(gqa, B, Hkv, g, Sq, Sk, D,
             launches += 1 + part.launches
             work += part.work_units
     assert plan.launches == launches and plan.work_units == work
+
+
+@pytest.mark.parametrize("g", [128, 129, 200, 256, 1000])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_token_of_many_heads_per_kv_head(gqa, g, D):
+    """More query heads per kv head than a 128-row tile holds: planned as the
+    16-bit library plans it, for one token; refused for more."""
+    rc, plan = _rc(gqa, _problem(gqa, 2, 3 * g, 3, 1, 500, D))
+    assert rc == 0 and gqa.KERNEL_NAMES[plan.kernel] == "q4"
+    assert plan.work_units == 2 * 3 * -(-g // 8) * 4
+    rc, _ = _rc(gqa, _problem(gqa, 2, 3 * g, 3, 2, 500, D))
+    assert rc == (0 if g <= 128 else 4)

@@ -613,3 +613,12 @@ def test_binding_refuses_on_the_gpu(gqa):
     assert gqa._lib.gqa_forward_q4(ctypes.byref(p), q.data_ptr(), c.data_ptr(), None, None,
                                    q.data_ptr(), None, 0, None) == gqa.GQA_ERR_NULL
     _ok(gqa)
+
+
+@pytest.mark.parametrize("dtype,g,Sk,D,lens", [
+    ("bf16", 32, 600, 128, None), ("fp16", 64, 300, 64, [300, 1]), ("bf16", 129, 77, 128, None),
+    ("fp16", 129, 1000, 128, [1000, 130]), ("bf16", 256, 400, 64, [3, 400]),
+    ("fp16", 200, 1, 40, None),
+])
+def test_one_token_of_many_heads_per_kv_head(gqa, dtype, g, Sk, D, lens):
+    _case(gqa, dtype, 2, 2 * g, 2, 1, Sk, D, seed=g + Sk, lens=lens)
