@@ -148,7 +148,7 @@ double decode_ns(const gqa_problem& p, const DecodeShape& s, int sms) {
 }
 
 double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
-  const double places = double(s.groups) * double((keys_read(p) + 127) / 128 + kQ4Lead);
+  const double places = double(s.groups) * double((keys_read(p) + 127) / 128 + kChunkLead);
   return kChunkNs + places / sms * (s.nq == 2 ? kChunkPairNs : kChunkTileNs);
 }
 

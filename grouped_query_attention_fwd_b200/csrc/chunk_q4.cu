@@ -891,7 +891,7 @@ ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count) {
   s.nq = s.m_tiles > 1 ? 2 : 1;
   s.m_groups = (s.m_tiles + s.nq - 1) / s.nq;
   s.groups = p.batch * p.heads_kv * s.m_groups;
-  s.places = s.groups * (s.tiles + kQ4Lead);
+  s.places = s.groups * (s.tiles + kChunkLead);
   const int64_t real = s.groups * s.tiles;
   s.grid = static_cast<int>(real < sm_count ? real : sm_count);
   const int rb = p.kv_lens != nullptr ? static_cast<int>(p.batch) : 0;
@@ -921,7 +921,7 @@ int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs
   ca.nq = s.nq;
   ca.m_groups = s.m_groups;
   ca.tiles = s.tiles;
-  ca.lead = kQ4Lead;
+  ca.lead = kChunkLead;
   ca.places = static_cast<int>(s.places);
   ca.stages = s.stages;
   ca.grid = s.grid;

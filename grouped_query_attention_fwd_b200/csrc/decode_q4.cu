@@ -25,15 +25,25 @@
 //    ldmatrix.trans of the 16-byte code blocks pairs the same halfword of two
 //    keys in one register, the layout of V^T as the A operand.
 //  * The weights p_j s_jg are rounded to fp16 (2^-11) as the B operand of
-//    P V in both cache types.  To keep them in fp16's range whatever the
-//    scales, the exponent reference is the running maximum of t_j + log2 of
-//    key j's largest V scale: the weights stay at or below 2^8.  With an
-//    fp16 cache the rounded weights are also summed (a row of ones in an MMA
-//    of its own) and eight of them taken off, so that the rounding multiplies
-//    codes counted from the middle of the group's range, at most half of it;
-//    bf16 outputs are rounded 8 times more coarsely than the weights as it is.
-//  * The reference is lazy: it moves, and the sums are rescaled, only when a
-//    score passes it by more than 2^8, which one vote per chunk finds out.
+//    P V in both cache types.  So that they use fp16's range whatever the
+//    scales, every row has a power of two per group of 32 dims on them, which
+//    is taken off the group's outputs at the end and brings the row's largest
+//    weight of the group so far to about 1: weights down to 2^-14 of it keep
+//    their 11 bits, and each is off by at most 2^-25 of it.  (One power for
+//    all groups, from each key's largest scale, is cheaper by a few percent and
+//    wrong: a group of values 2^20 times smaller than its neighbours' comes out
+//    4% off.)
+//  * Both the exponent reference m and the powers are lazy.  They are taken
+//    anew when a score passes m by more than 2^6 or a key's scale is more than
+//    2^9 times what the group's power stands for, so that a weight stays below
+//    2^15; one vote per chunk finds out.  m is a whole number: it moves by
+//    powers of two, which the groups' powers take up, so that the products'
+//    sums stay as they are.
+//  * With an fp16 cache the rounded weights are also summed (a row of ones in
+//    an MMA of its own) and eight of them taken off, so that the rounding
+//    multiplies codes counted from the middle of the group's range, at most
+//    half of it; bf16 outputs are rounded 8 times more coarsely than the
+//    weights as it is.
 //
 // Reads 160 bytes per key of 128 dims against 512 in 16 bits.  Bound: issue
 // slots of the unpacking and the softmax, then HBM: 16 entries of 32768 keys,
@@ -59,7 +69,11 @@ namespace {
 using namespace q4;
 
 constexpr int KT = kDecodeKeysPerTile;
-constexpr float kLazyLog2 = 8.0f;          // the reference may trail a score by 2^8
+// Powers of two that a score may pass the exponent reference by, and a value
+// scale the row's largest weight of its group, before they are taken anew: their
+// product has to stay in fp16 (2^15).
+constexpr int kLazyLog2 = 6, kLazyScaleLog2 = 9;
+constexpr uint32_t kPowerMost = 100;  // of a group: no weight yet
 constexpr int kFastMerge = 4;              // contributors of a split group merged directly
 constexpr int kBatch = 8;                  // partials loaded at a time by the other merge
 // How many units longer than equal ranges the ranges may be that no two groups
@@ -122,10 +136,31 @@ __device__ __forceinline__ void ldmatrix_x2(uint32_t& r0, uint32_t& r1, uint32_t
                : "r"(addr));
 }
 
-__device__ __forceinline__ float fast_lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+// 2^e, e in [-127, 127] (2^-127: 0), and the exponent of a power of two or of
+// any other positive number, rounded down (below 2^-126: -127).
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+__device__ __forceinline__ int exponent_of(float x) {
+  return static_cast<int>(__float_as_uint(x) >> 23) - 127;
+}
+
+// 2^e in the cache's type, rounded down where it has none: 0 or infinity.
+template <bool F16>
+__device__ __forceinline__ uint32_t type_power(int e) {
+  constexpr int kBias = F16 ? 15 : 127, kBits = F16 ? 10 : 7;
+  return static_cast<uint32_t>(min(max(e + kBias, 0), 2 * kBias + 1)) << kBits;
+}
+
+// Larger of two pairs of 16-bit numbers; of a NaN and a number, the number.
+template <bool F16>
+__device__ __forceinline__ uint32_t max_number(uint32_t x, uint32_t y) {
+  uint32_t r;
+  if (F16)
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  else
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
 }
 
 // Record heads: NG words (scale | minimum << 16).
@@ -751,8 +786,11 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
       for (int e = 0; e < 2; ++e)
         vis_at[e] = (!MQ ? 0 : (a.Sq < HP ? (2 * c + e) % a.Sq : 2 * c + e)) * (KT / 32);
 
-      float o[NG][2][4], corr[NG][2];
+      float o[NG][2][4];
+      uint64_t corr[NG];  // of both rows
       float osum[4];  // fp16: lanes 4 t + c hold group t's summed weights
+      uint64_t pow[NG];   // both rows' powers of two on the groups' weights, in o and osum
+      uint32_t limit[NG / 2];  // value scales that they allow, two groups to a word
       // The exponent reference (running maximum), its negative with 0 for
       // -inf, the score above which it moves, and the sum of the weights.
       float m_ref[2], m_neg[2], m_top[2], l[2];
@@ -764,7 +802,9 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
         m_neg[e] = l[e] = 0.f;
 #pragma unroll
         for (int t = 0; t < NG; ++t) {
-          corr[t][e] = 0.f;
+          corr[t] = 0;
+          pow[t] = f2_pack(0x1p100f, 0x1p100f);
+          limit[t / 2] = 0u;
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[t][e][x] = 0.f;
         }
@@ -845,21 +885,6 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
               sv[j][y] = fmaf(scale_of<F16>(kp[y >> 1][t]), acc[y], sv[j][y]);
           }
         }
-        // log2 of each key's largest V scale (see the top), within 2^-60 .. 2^100.
-        float lsv[kSub][2];
-#pragma unroll
-        for (int j = 0; j < kSub; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t w[NG];
-            load_params<NG>(w, vb + (j * 16 + k * 8 + r8) * P);
-            float m = 0x1p-60f;
-#pragma unroll
-            for (int t = 0; t < NG; t += 2)
-              m = fmax3(m, scale_of<F16>(w[t]), scale_of<F16>(w[t + 1]));
-            lsv[j][k] = fast_lg2(fminf(m, 0x1p100f));
-          }
-
         auto rest = [&](auto all_seen) {
           constexpr bool kWhole = decltype(all_seen)::value;
           // Scores in base 2 are sv * fac; with hidden keys the product is
@@ -875,36 +900,110 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
               seen[j][y] =
                   kWhole || ((vis[e][j >> 1] >> (r8 + 16 * (j & 1) + 8 * (y >> 1))) & 1u) != 0u;
               if (!kWhole) t = seen[j][y] ? t * fac[e] : -INFINITY;
-              raise |= fmaf(t, kWhole ? fac[e] : 1.f, lsv[j][y >> 1]) > m_top[e];
+              raise |= (kWhole ? t * fac[e] : t) > m_top[e];
             }
+          // The largest scales of the values, against what the powers allow.
+          {
+            uint32_t most[NG];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t w[NG];
+                load_params<NG>(w, vb + (j * 16 + 8 * k + r8) * P);
+#pragma unroll
+                for (int t = 0; t < NG; ++t)
+                  most[t] = j + k == 0 ? w[t] : max_number<F16>(most[t], w[t]);
+              }
+#pragma unroll
+            for (int t = 0; t < NG; t += 2)
+              raise |= max_number<F16>(__byte_perm(most[t], most[t + 1], 0x5410), limit[t / 2]) !=
+                       limit[t / 2];
+          }
           if (__any_sync(0xffffffffu, raise)) {
+            // The reference goes to the maximum, rounded up; l and corr follow by
+            // alpha (0 for a row without a key so far).  Powers of two are kept as
+            // the bits of their exponent.
+            const bool begun = __any_sync(0xffffffffu, m_ref[0] > -INFINITY || m_ref[1] > -INFINITY);
+            float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float f = kWhole ? fac[e] : 1.f;
               float mx = -INFINITY;
 #pragma unroll
-              for (int j = 0; j < kSub; ++j)
-                mx = fmax3(mx, fmaf(sv[j][e], f, lsv[j][0]), fmaf(sv[j][2 + e], f, lsv[j][1]));
+              for (int j = 0; j < kSub; ++j) mx = fmax3(mx, sv[j][e] * f, sv[j][2 + e] * f);
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float m_new = fmaxf(m_ref[e], mx);
+              const float m_new = ceilf(fmaxf(m_ref[e], mx));
+              alpha[e] = power_of_two(static_cast<int>(fmaxf(m_ref[e] - m_new, -127.f)));
               m_neg[e] = -exp_ref(m_new);
-              const float alpha = fast_exp2(m_ref[e] + m_neg[e]);
               m_ref[e] = m_new;
-              m_top[e] = m_new + kLazyLog2;
-              l[e] *= alpha;
-              if (F16) osum[e] *= alpha;
+              m_top[e] = m_new + float(kLazyLog2);
+            }
+            // This chunk's largest weight of each group, as bf16 pairs of rows.
+            uint32_t most[NG];
 #pragma unroll
-              for (int t = 0; t < NG; ++t) {
-                corr[t][e] *= alpha;
+            for (int j = 0; j < kSub; ++j)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                  o[t][u][e] *= alpha;
-                  o[t][u][2 + e] *= alpha;
+              for (int k = 0; k < 2; ++k) {
+                uint32_t w[NG];
+                load_params<NG>(w, vb + (j * 16 + 8 * k + r8) * P);
+                float pe[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  pe[e] = fast_exp2(fmaf(sv[j][2 * k + e], kWhole ? fac[e] : 1.f, m_neg[e]));
+#pragma unroll
+                for (int t = 0; t < NG; ++t) {
+                  const float scale = scale_of<F16>(w[t]);
+                  const uint64_t ww = f2_mul(f2_pack(pe[0], pe[1]), f2_pack(scale, scale));
+                  const uint32_t x =
+                      pack_bf16x2(kWhole || seen[j][2 * k] ? f2_lo(ww) : 0.f,
+                                  kWhole || seen[j][2 * k + 1] ? f2_hi(ww) : 0.f);
+                  most[t] = max_number<false>(j + k == 0 ? 0u : most[t], x);
                 }
               }
+#pragma unroll
+            for (int i = 4; i < 32; i <<= 1)
+#pragma unroll
+              for (int t = 0; t < NG; ++t)
+                most[t] = max_number<false>(most[t], __shfl_xor_sync(0xffffffffu, most[t], i));
+            // The powers follow the reference, as far as the largest weight (and
+            // 2^kPowerMost) allows, and o and osum what is left.
+#pragma unroll
+            for (int t = 0; t < NG; ++t) {
+              uint32_t to[2], high = 0u;
+              float by[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                constexpr uint32_t kOne = 127u << 23;
+                const uint32_t old = __float_as_uint(e ? f2_hi(pow[t]) : f2_lo(pow[t]));
+                const uint32_t back = old + kOne - __float_as_uint(alpha[e]);  // old / alpha
+                const uint32_t weight = (e ? most[t] : most[t] << 16) & 0x7F800000u;
+                to[e] = min(min(back, (127u + kPowerMost) << 23),
+                            2u * kOne - min(weight, 253u << 23));
+                by[e] = alpha[e] > 0.f && to[e] + kOne > back
+                            ? __uint_as_float(to[e] + kOne - back)
+                            : 0.f;
+                if (m_ref[e] > -INFINITY) high = max(high, to[e]);
+              }
+              const uint32_t code = type_power<F16>(kLazyScaleLog2 + 127 - static_cast<int>(high >> 23));
+              limit[t / 2] = t % 2 == 0 ? code : limit[t / 2] | (code << 16);
+              pow[t] = f2_pack(__uint_as_float(to[0]), __uint_as_float(to[1]));
+              if (begun) {
+                corr[t] = f2_mul(corr[t], f2_pack(alpha[0], alpha[1]));
+                if (F16 && r8 == t) {
+                  osum[0] *= by[0];
+                  osum[1] *= by[1];
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) o[t][u][y] *= by[y & 1];
+              }
             }
+            l[0] *= alpha[0];
+            l[1] *= alpha[1];
           }
 #pragma unroll
           for (int j = 0; j < kSub; ++j) {
@@ -928,18 +1027,18 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
                 const float scale = scale_of<F16>(vp[k][t]);
                 float add = min_of<F16>(vp[k][t]);
                 if (F16) add = fmaf(8.f, scale, add);
-                const float p0 = sv[j][2 * k], p1 = sv[j][2 * k + 1];
-                float w0 = p0 * scale, w1 = p1 * scale;
+                const uint64_t pp = f2_pack(sv[j][2 * k], sv[j][2 * k + 1]);
+                // (In this order: a weight of zero stays one.)
+                const uint64_t ww = f2_mul(f2_mul(pp, pow[t]), f2_pack(scale, scale));
                 if (kWhole) {
-                  corr[t][0] = fmaf(p0, add, corr[t][0]);
-                  corr[t][1] = fmaf(p1, add, corr[t][1]);
+                  corr[t] = f2_fma(pp, f2_pack(add, add), corr[t]);
+                  pb[k] = movmatrix_trans(pack_f16x2(f2_lo(ww), f2_hi(ww)));
                 } else {  // a hidden key's parameters may be NaN
-                  w0 = seen[j][2 * k] ? w0 : 0.f;
-                  w1 = seen[j][2 * k + 1] ? w1 : 0.f;
-                  corr[t][0] += seen[j][2 * k] ? p0 * add : 0.f;
-                  corr[t][1] += seen[j][2 * k + 1] ? p1 * add : 0.f;
+                  const bool s0 = seen[j][2 * k], s1 = seen[j][2 * k + 1];
+                  const uint64_t pa = f2_mul(pp, f2_pack(add, add));
+                  corr[t] = f2_add(corr[t], f2_pack(s0 ? f2_lo(pa) : 0.f, s1 ? f2_hi(pa) : 0.f));
+                  pb[k] = movmatrix_trans(pack_f16x2(s0 ? f2_lo(ww) : 0.f, s1 ? f2_hi(ww) : 0.f));
                 }
-                pb[k] = movmatrix_trans(pack_f16x2(w0, w1));
               }
               const uint32_t v0 = vw[t][0] >> 8, v1 = vw[t][1] >> 8;
               mma_f16_16816(o[t][0], vw[t][0] & 0x000F000Fu, vw[t][0] & 0x00F000F0u,
@@ -995,14 +1094,15 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
         for (int i = 4; i < 32; i <<= 1) lv += __shfl_xor_sync(0xffffffffu, lv, i);
 #pragma unroll
         for (int t = 0; t < NG; ++t) {
-          float cv = corr[t][e];
+          float cv = e ? f2_hi(corr[t]) : f2_lo(corr[t]);
 #pragma unroll
           for (int i = 4; i < 32; i <<= 1) cv += __shfl_xor_sync(0xffffffffu, cv, i);
-          if (F16) cv -= 8.f * __shfl_sync(0xffffffffu, osum[e], 4 * t + c);
-          // Codes carry 2^-24, those of odd nibbles 2^-20.
-          *reinterpret_cast<float4*>(row + 32 * t + 4 * r8) =
-              make_float4(fmaf(o[t][0][e], 0x1p24f, cv), fmaf(o[t][0][2 + e], 0x1p20f, cv),
-                          fmaf(o[t][1][e], 0x1p24f, cv), fmaf(o[t][1][2 + e], 0x1p20f, cv));
+          const float off = power_of_two(-exponent_of(e ? f2_hi(pow[t]) : f2_lo(pow[t])));
+          if (F16) cv = fmaf(-8.f * off, __shfl_sync(0xffffffffu, osum[e], 4 * t + c), cv);
+          // Codes carry 2^-24, those of odd nibbles 2^-20, and the group's power.
+          *reinterpret_cast<float4*>(row + 32 * t + 4 * r8) = make_float4(
+              fmaf(o[t][0][e] * 0x1p24f, off, cv), fmaf(o[t][0][2 + e] * 0x1p20f, off, cv),
+              fmaf(o[t][1][e] * 0x1p24f, off, cv), fmaf(o[t][1][2 + e] * 0x1p20f, off, cv));
         }
         if (r8 == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m_ref[e], lv);
       }

@@ -276,7 +276,7 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
 // a split group's partials; and what a change of groups inside a range costs,
 // in units.
 constexpr double kQ4UnitNs = 550, kQ4MergeNs = 2500;
-constexpr int kQ4Lead = 6;
+constexpr int kQ4Lead = 8, kChunkLead = 6;
 constexpr int kQ4Threads = 384;
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
@@ -290,7 +290,7 @@ struct ChunkShape {
   int nq, m_groups;   // query tiles per group (1 or 2); ceil(m_tiles / nq)
   int tiles;          // key tiles per group; with kv_lens, the most
   int64_t groups;     // batch * heads_kv * m_groups
-  int64_t places;     // groups * (tiles + kQ4Lead)
+  int64_t places;     // groups * (tiles + kChunkLead)
   int grid, stages, smem_bytes;
   bool fits;          // the kernel takes the problem
   int64_t info_offset, part_ml_offset, part_o_offset, workspace_end;

@@ -622,3 +622,62 @@ def test_binding_refuses_on_the_gpu(gqa):
 ])
 def test_one_token_of_many_heads_per_kv_head(gqa, dtype, g, Sk, D, lens):
     _case(gqa, dtype, 2, 2 * g, 2, 1, Sk, D, seed=g + Sk, lens=lens)
+
+
+def _group_factors(pattern, ratio, S, G, t):
+    """Powers of two on the values of each (key, group of 32 dims), [S, G]."""
+    f = np.ones((S, G))
+    r = 2.0 ** round(np.log2(ratio) / 2)
+    if pattern == "apart":           # one group far above, one far below the others
+        f[:, 0], f[:, 1] = r, 1.0 / r
+    elif pattern == "outlier":       # the keys that matter least hold large values in one group
+        f[np.argsort(t)[:S // 8], 0] = ratio
+    elif pattern == "turns":         # keys in turn, and late keys of other sizes
+        f[0::2, 0], f[1::2, 1] = r, 1.0 / r
+        f[S // 2:] /= r
+    return f
+
+
+@pytest.mark.parametrize("Sq", [1, 2])
+@pytest.mark.parametrize("pattern", ["apart", "outlier", "turns"])
+@pytest.mark.parametrize("dtype,ratio,D", [
+    ("bf16", 2.0 ** 10, 128), ("bf16", 2.0 ** 20, 128), ("bf16", 2.0 ** 30, 64),
+    ("bf16", 2.0 ** 60, 128), ("fp16", 2.0 ** 10, 128), ("fp16", 2.0 ** 16, 64),
+    ("fp16", 2.0 ** 20, 128),
+])
+def test_groups_of_different_sizes(gqa, dtype, ratio, D, pattern, Sq):
+    """Each group of 32 dims keeps its own relative precision, whatever its
+    neighbours' values are, and whichever keys hold the large ones."""
+    if dtype == "fp16" and pattern == "outlier" and ratio > 2.0 ** 10:
+        pytest.skip("values past fp16's range")
+    rng = np.random.default_rng(int(np.log2(ratio)) + D)
+    B, H, g, S, G = 1, 2, 3, 3000, -(-D // 32)
+    q = rng.standard_normal((B, H * g, Sq, D)).astype(np.float32) * 3
+    k = rng.standard_normal((B, H, S, D)).astype(np.float32)
+    qb, kb = u.bits_of(q, dtype), u.bits_of(k, dtype)
+    krec = u.quantise(kb, dtype)
+    q64, k64 = u.values_of(qb, dtype), u.dequantise(krec, D, dtype)
+    t = (q64[0, 0, 0] @ k64[0, 0].T)
+    f = np.repeat(_group_factors(pattern, ratio, S, G, t), 32, -1)[:, :D]
+    v = rng.standard_normal((B, H, S, D)) * f
+    vrec = u.quantise(u.bits_of(v, dtype), dtype)
+    v64 = u.dequantise(vrec, D, dtype)
+    assert np.all(np.isfinite(v64))
+    out = u.to64(gqa.forward_q4(u.dev16(qb, dtype), torch.from_numpy(krec).cuda(),
+                                torch.from_numpy(vrec).cuda()))
+    _ok(gqa)
+    ref = oracle.forward(q64, k64, v64)
+    p = _probs(q64, k64, None, g).reshape(B, H, g * Sq, S)
+    # Roundings: each weight once to fp16, half a step of 2^-11 of it, times
+    # codes of at most 15 scales (fp16 caches: 8, from the middle) and at least
+    # 2^-32 of the row's largest weight of the group; fp32 sums and exponents,
+    # 2^-14 of the terms; the result once (fp16's subnormal step: 2^-25).
+    s = np.repeat(u.parts(vrec, D, dtype)[0], u.GROUP, -1)[..., :D]
+    far = 15 if dtype == "bf16" else 8
+    ps = np.einsum("bhrs,bhsd->bhrsd", p, s)
+    lost = S * 2.0 ** -32 * ps.max(3)
+    bound = far * (2.0 ** -11 * ps.sum(3) + lost) + \
+        2.0 ** -14 * np.einsum("bhrs,bhsd->bhrd", p, np.abs(v64) + far * s)
+    bound = bound.reshape(B, H * g, Sq, D) + 1.01 * u.UNIT[dtype] * np.abs(ref) + 2.0 ** -25
+    err = np.abs(out - ref)
+    assert np.all(err <= bound), float((err / bound).max())
