@@ -337,7 +337,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto page_of = [&](int nt) {
           const int key = nt * BN + (lane & 1) * 64;
           if (nt >= me.nt_end || key >= me.pr.len) return pg.num_pages;
-          const int page = __ldg(pg.bt + me.pr.b * pg.bt_stride + key / pg.page_size);
+          // (From L2: an earlier kernel may have written it while this one was resident.)
+          const int page = __ldcg(pg.bt + me.pr.b * pg.bt_stride + key / pg.page_size);
           if (page >= 0 && page < pg.num_pages) return page;
           atomicOr(a.err, kErrPage);
           return pg.num_pages;  // out of range: read as zeros
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(256)
   griddep_launch_dependents();
   griddep_wait();
   const int id = blockIdx.x;
-  const int2 info = ca.info[id];
+  const int2 info = __ldcg(&ca.info[id]);  // (L2: resident before these were written)
   // (Anything else than slots of the launch: it was aborted before writing.)
   if (info.y <= 1 || info.x < 0 || info.y > ca.grid || info.x / 2 > ca.grid - info.y) return;
   const int lane = threadIdx.x & 31;
@@ -800,7 +801,7 @@ __global__ void __launch_bounds__(256)
       return (static_cast<int64_t>(k == 0 ? info.x : (info.x / 2 + k) * 2) * ca.nq + X) * BM + row;
     };
     float M = -INFINITY;
-    for (int k = lane; k < info.y; k += 32) M = fmaxf(M, ca.part_ml[at(k)].x);
+    for (int k = lane; k < info.y; k += 32) M = fmaxf(M, __ldcg(&ca.part_ml[at(k)]).x);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, i));
     const float ref = exp_ref(M);
@@ -808,8 +809,8 @@ __global__ void __launch_bounds__(256)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < info.y; ++k) {
-      const float2 ml = ca.part_ml[at(k)];
-      const float4 o = *reinterpret_cast<const float4*>(ca.part_o + at(k) * D + d);
+      const float2 ml = __ldcg(&ca.part_ml[at(k)]);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(ca.part_o + at(k) * D + d));
       const float w = fast_exp2(ml.x - ref);
       l = fmaf(w, ml.y, l);
       acc.x = fmaf(w, o.x, acc.x);

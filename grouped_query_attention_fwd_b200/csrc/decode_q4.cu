@@ -68,6 +68,11 @@ namespace {
 
 using namespace q4;
 
+// Loads of what an earlier kernel of the stream may have written (the mask and
+// its bits, the block table, partials) go to L2: as a programmatic dependent
+// this kernel can be resident before those writes, so that neither the
+// non-coherent path nor a line in L1 is good for them.
+
 constexpr int KT = kDecodeKeysPerTile;
 // Powers of two that a score may pass the exponent reference by, and a value
 // scale the row's largest weight of its group, before they are taken anew: their
@@ -184,7 +189,7 @@ constexpr int kMaskSpan = 1024;  // keys a warp packs at a time, a word per lane
 // its producer or its consumers, they cost it more than the records (8 x 6001
 // keys, four queries: 100 and 55 us against 32 without a mask).
 __global__ void __launch_bounds__(256)
-    gqa_q4_mask_bits_kernel(const DecodeArgs a, uint32_t* __restrict__ bits) {
+    gqa_q4_mask_bits_kernel(const DecodeArgs a, uint32_t* bits) {
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
@@ -201,7 +206,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
         const int64_t key = k0 + 32 * (w0 + w) + lane;
-        on[w] = key < a.Sk ? __ldg(m + key) : 0;
+        on[w] = key < a.Sk ? __ldcg(m + key) : 0;
       }
 #pragma unroll
       for (int w = 0; w < 8; ++w) {
@@ -220,8 +225,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
                          const __grid_constant__ CUtensorMap tmv, const DecodeArgs a,
                          const int tiles_per_group, const int passes, const int units,
                          const int stages, const int split, const int lead,
-                         const uint32_t* __restrict__ mask_bits,
-                         uint32_t* __restrict__ counters) {
+                         const uint32_t* mask_bits, uint32_t* counters) {
   using L = Q4Layout<NG>;
   constexpr int HP = L::HP, D = L::D, W = L::W, P = L::kPitch, R = L::kRow;
   constexpr int kSub = L::kSub, kChunk = L::kChunk, kChunks = L::kChunks;
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
       // page num_pages, which is out of range: TMA fills it with zeros.
       auto page_of = [&](int key, bool wanted) {
         if (!wanted || key >= len) return a.num_pages;
-        const int page = __ldg(a.bt + b * a.bt_stride + key / a.page_size);
+        const int page = __ldcg(a.bt + b * a.bt_stride + key / a.page_size);
         if (page >= 0 && page < a.num_pages) return page;
         atomicOr(a.err, kErrPage);
         return a.num_pages;  // read as zeros
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
           }
           // Mask bits of the unit's 128 keys, lane 4 i + w: query i of the pass,
           // keys 32 w .. + 31.  (Read before the wait for a free stage.)
-          const uint32_t bits = my_bits != nullptr ? __ldg(my_bits + key0 / 32) : 0u;
+          const uint32_t bits = my_bits != nullptr ? __ldcg(my_bits + key0 / 32) : 0u;
           // (Every lane waits: the warp stays converged.)
           ok = __all_sync(0xffffffffu, mbar_try_wait(&empty[s], parity) ||
                                            mbar_wait(&empty[s], parity, abort_flag, a.err,

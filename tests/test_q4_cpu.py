@@ -249,3 +249,19 @@ def test_one_token_of_many_heads_per_kv_head(gqa, g, D):
     assert plan.work_units == 2 * 3 * -(-g // 8) * 4
     rc, _ = _rc(gqa, _problem(gqa, 2, 3 * g, 3, 2, 500, D))
     assert rc == (0 if g <= 128 else 4)
+
+
+def test_no_non_coherent_loads():
+    """The kernels over records start while earlier kernels of the stream still
+    write what they read (masks, block tables, lengths, partials): none of it
+    may go through the read-only path, which promises that nothing writes."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                        "grouped_query_attention_fwd_b200", "csrc")
+    sources = glob.glob(os.path.join(csrc, "*q4*"))
+    assert len(sources) >= 5
+    for path in sources:
+        text = open(path).read()
+        assert not re.search(r"__ldg\s*\(|\.nc\.|__restrict__", text), path
