@@ -1207,13 +1207,18 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
           merge_warps(hr, d4, M, lsum, acc);
           float top = M;
 #pragma unroll
-          for (int k = 0; k < kFastMerge; ++k) top = fmaxf(top, ml[k].x);
-          const float ref = exp_ref(top), own = fast_exp2(M - ref);
-          lsum *= own;
-          acc.x *= own;
-          acc.y *= own;
-          acc.z *= own;
-          acc.w *= own;
+          for (int k = 0; k < kFastMerge; ++k) {
+            if (grp.c_lo + k == static_cast<int>(blockIdx.x)) {
+              ml[k] = make_float2(M, lsum);
+              ov[k] = acc;
+            }
+            top = fmaxf(top, ml[k].x);
+          }
+          // In merge_partials' order, so that the result's bits do not depend
+          // on which of the two came to merge.
+          const float ref = exp_ref(top);
+          lsum = 0.f;
+          acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < kFastMerge; ++k) {
             const float w = fast_exp2(ml[k].x - ref);

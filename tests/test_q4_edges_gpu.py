@@ -216,3 +216,28 @@ def test_wait_runs_out_and_is_reported(gqa, unit):
     out = gqa.forward_q4(q, ck, cv, workspace=ws)
     assert gqa.device_status(ws) == gqa.GQA_OK
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,S,D,lens", [
+    (16, 32, 8, 4096, 128, None),
+    (5, 40, 8, 6000, 64, None),
+    (9, 32, 8, 4000, 128, [4000, 100, 2500, 3999, 1, 3000, 777, 1500, 2048]),
+])
+def test_same_bits_whoever_merges(gqa, B, Hq, Hkv, S, D, lens):
+    """Which CTA merges a split group's partials, and in which of two ways, is
+    a matter of timing, which other work on the machine changes; the sums are
+    taken in one order."""
+    ck, cv = _cache(gqa, B, Hkv, S, D, torch.float16)
+    q = _q(B, Hq, 1, D, torch.float16)
+    kw = {} if lens is None else dict(kv_lens=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    want = gqa.forward_q4(q, ck, cv, **kw)
+    side, x = torch.cuda.Stream(), torch.zeros(1 << 24, device="cuda")
+    torch.cuda.synchronize()
+    outs = []
+    for i in range(300):
+        if i % 3 == 0:
+            with torch.cuda.stream(side):
+                x[: 1 << (10 + i % 15)].add_(1.0)
+        outs.append(gqa.forward_q4(q, ck, cv, **kw))
+    assert gqa.device_status() == gqa.GQA_OK
+    assert all(torch.equal(o, want) for o in outs)
