@@ -505,15 +505,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             par[i] = ld_shared(raw_at + s * L::kRaw + (half * G2 + i) * 4);
             code[i] = ld_shared4(raw_at + s * L::kRaw + kHeadBytes + (half * G2 + i) * 16);
           }
-          // The stage is handed back once its words have come: a load only
-          // issued may wait behind the products' operand reads until the next
-          // copy has landed (seen: results that changed from call to call).
-          // Branching on the words waits for them; the branch itself does nothing.
+          // The stage goes back to the producer, whose next copy overwrites it.
+          // Three things stand between the loads above and that copy: the loads
+          // are generic accesses and the copy is one of the async proxy, which
+          // the mbarrier alone does not order (the proxy fence); they are 32
+          // lanes' and the arrival is lane 0's (__syncwarp, which a vote does not
+          // replace); and the words are in registers (the branch, never taken).
+          // Without the fence and the branch, results at head dim 128 changed
+          // from call to call.
           uint32_t any = 0u;
 #pragma unroll
           for (int i = 0; i < G2; ++i)
             any ^= par[i] ^ code[i].x ^ code[i].y ^ code[i].z ^ code[i].w;
           if (__any_sync(0xffffffffu, any == 0xA5A5A5A5u)) __nanosleep(0);
+          fence_proxy_async_smem();
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < G2; ++i)
             if (!held) par[i] = 0u;  // past the length: zeros

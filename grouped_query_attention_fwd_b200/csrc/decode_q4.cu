@@ -1055,8 +1055,11 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
               }
             }
           }
-          // Handed back when every word has been used: a load that has only
-          // been issued is no proof that it has come.
+          // The stage goes back when every word of it is in registers (the
+          // products above have used them), with every lane's loads before
+          // lane 0's arrival and, by the proxy fence, before the next copy, an
+          // access of the async proxy that the mbarrier alone does not order.
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[s]);
         };
