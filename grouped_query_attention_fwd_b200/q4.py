@@ -52,7 +52,8 @@ _lib.gqa_forward_q4.restype = ctypes.c_int
 
 # Checked descriptors, per thread (a call writes its pointers into the one it
 # uses).  The key is everything that the checks look at: types, devices, sizes,
-# strides and scalars of every argument, never an address.
+# strides of every tensor, never an address, and the scalars as plain numbers
+# (a 0-d tensor is one by its value, not by its identity).
 _seen = threading.local()
 _MAX_SEEN = 1024
 
@@ -212,6 +213,7 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
         with away:
             return kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens, advance,
                                 workspace, None, block_table)
+    advance = bool(advance)
     key = (_like(k_new), _like(v_new), _like(cache_k), _like(cache_v), _like(kv_lens),
            None if new_lens is None else _like(new_lens),
            None if block_table is None else _like(block_table), advance)
@@ -228,7 +230,7 @@ def kv_append_q4(cache_k, cache_v, k_new, v_new, kv_lens, new_lens=None, advance
         _check_int32(new_lens, B, "new_lens")
         _check_int32(kv_lens, B, "kv_lens")
         d = _remember(seen, key, _rows_desc(k_new.dtype, cache_k, cache_v, k_new, v_new,
-                                            k_new.shape[3], block_table, bool(advance)))
+                                            k_new.shape[3], block_table, advance))
     d.block_table = _ptr(block_table)
     d.counts = _ptr(new_lens)
     handle = _stream_now(idx)
@@ -256,6 +258,7 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
                               workspace, None, block_table)
     starts = start if isinstance(start, torch.Tensor) else None
     start = 0 if starts is not None else int(start)
+    head_dim, n = int(head_dim), None if n is None else int(n)
     key = (dtype, head_dim, n, start if n is None else None, _like(cache_k), _like(cache_v),
            None if kv_lens is None else _like(kv_lens), None if starts is None else _like(starts),
            None if out_k is None else _like(out_k), None if out_v is None else _like(out_v),
@@ -272,10 +275,10 @@ def kv_read_q4(cache_k, cache_v, head_dim, dtype, kv_lens=None, start=0, n=None,
             capacity *= block_table.shape[1]
         _check_int32(starts, B, "start")
         _check_int32(kv_lens, B, "kv_lens")
-        count = int(n) if n is not None else capacity - start
+        count = n if n is not None else capacity - start
         if count < 0:
             raise ValueError("n must not be negative")
-        shape = (B, Hkv, count, int(head_dim))
+        shape = (B, Hkv, count, head_dim)
         for t in (out_k, out_v):
             if t is not None and (t.shape != shape or t.dtype is not dtype):
                 raise ValueError("out_k and out_v must be [B, Hkv, n, D] of the given type")
@@ -371,6 +374,10 @@ def forward_q4(q, cache_k, cache_v, mask=None, causal=False, scale=None, out=Non
         with away:
             return forward_q4(q, cache_k, cache_v, mask, causal, scale, out, workspace, None,
                               causal_offset, window, kv_lens, block_table)
+    causal, window = bool(causal), int(window)
+    scale = None if scale is None else float(scale)
+    if causal_offset is not None and not isinstance(causal_offset, str):
+        causal_offset = int(causal_offset)
     key = (_like(q), _like(cache_k), _like(cache_v), None if mask is None else _like(mask),
            None if kv_lens is None else _like(kv_lens),
            None if block_table is None else _like(block_table),

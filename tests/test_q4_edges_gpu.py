@@ -218,6 +218,29 @@ def test_wait_runs_out_and_is_reported(gqa, unit):
     assert torch.equal(out, want)
 
 
+def test_scalars_written_again(gqa):
+    """Scalars given as 0-d tensors count by their value at each call."""
+    ck, cv = _cache(gqa, 2, 2, 200, 64)
+    q = _q(2, 4, 3, 64)
+    scale, window, offset = torch.tensor(0.125), torch.tensor(50), torch.tensor(197)
+    n, D = torch.tensor(5), torch.tensor(64)
+    for s, w, o, t in ((0.125, 50, 197, 5), (0.5, 50, 197, 6), (0.5, 7, 197, 6), (0.5, 7, 100, 4)):
+        scale.fill_(s), window.fill_(w), offset.fill_(o), n.fill_(t)
+        got = gqa.forward_q4(q, ck, cv, causal=True, scale=scale, window=window,
+                             causal_offset=offset)
+        want = gqa.forward_q4(q, ck, cv, causal=True, scale=s, window=w, causal_offset=o)
+        assert torch.equal(got, want)
+        k, _ = gqa.kv_read_q4(ck, cv, D, torch.bfloat16, start=3, n=n)
+        assert torch.equal(k, gqa.kv_read_q4(ck, cv, 64, torch.bfloat16, start=3, n=t)[0])
+    lens, on = torch.tensor([10, 20], dtype=torch.int32, device="cuda"), torch.tensor(True)
+    new = _q(2, 2, 1, 64, seed=9)
+    gqa.kv_append_q4(ck, cv, new, new, lens, advance=on)
+    on.fill_(False)
+    gqa.kv_append_q4(ck, cv, new, new, lens, advance=on)
+    assert lens.tolist() == [11, 21]
+    assert gqa.device_status() == gqa.GQA_OK
+
+
 @pytest.mark.parametrize("B,Hq,Hkv,S,D,lens", [
     (16, 32, 8, 4096, 128, None),
     (5, 40, 8, 6000, 64, None),
