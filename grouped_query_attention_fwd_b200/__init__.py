@@ -180,7 +180,7 @@ def _torch():
 
 
 _workspaces = {}
-_replaced_workspaces = []  # outgrown ones: a captured graph may still point at one
+_captured_workspaces = {}  # those that a graph capture was given, by address: a graph points at them
 
 
 def _dtype_code(t) -> int:
@@ -293,7 +293,10 @@ def workspace_for(device, nbytes: int, stream=None):
     ordered on one stream, since the split-merge counters it holds are not
     safe for calls that overlap on the GPU.  A new workspace is allocated and
     zero-filled on that stream, so the caching allocator orders its reuse
-    after the stream's earlier work."""
+    after the stream's earlier work.  It is larger than asked for by up to as
+    much again (64 MB at most), so that sizes that grow step by step do not
+    each make one; the outgrown one is given back, unless a capture of the
+    stream was handed it."""
     torch = _torch()
     dev = torch.device(device)
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
@@ -301,12 +304,28 @@ def workspace_for(device, nbytes: int, stream=None):
     key = (idx, int(st.cuda_stream))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        with torch.cuda.device(idx), torch.cuda.stream(st):
-            new = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
+        size = max(nbytes, 256)
         if ws is not None:
-            _replaced_workspaces.append(ws)
-        _workspaces[key] = ws = new
+            size = max(size, min(2 * ws.numel(), ws.numel() + _GROWTH))
+        with torch.cuda.device(idx), torch.cuda.stream(st):
+            ws = torch.zeros(size, dtype=torch.uint8, device=torch.device("cuda", idx))
+        _workspaces[key] = ws
+    if _capturing(st, idx):
+        _captured_workspaces[ws.data_ptr()] = ws
     return ws
+
+
+_GROWTH = 64 << 20  # bytes that a workspace grows by beyond what is asked for, at most
+
+
+def _capturing(st, idx) -> bool:
+    """Whether ``st``, a stream of device ``idx``, is being captured into a graph."""
+    torch = _torch()
+    c = torch._C
+    if c._cuda_getDevice() == idx and c._cuda_getCurrentRawStream(idx) == st.cuda_stream:
+        return c._cuda_isCurrentStreamCapturing()
+    with torch.cuda.device(idx), torch.cuda.stream(st):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def forward(q, k, v, mask=None, causal=False, scale=None, out=None, workspace=None,
