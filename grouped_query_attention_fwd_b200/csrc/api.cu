@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "gqa.h"
+#include "enqueue_turn.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -294,11 +295,6 @@ int encode_decode_kv_map(CUtensorMap* map, const void* base, const gqa_problem& 
                          kDecodeKeysPerTile, 1, f16);
 }
 
-std::mutex& enqueue_mutex() {
-  static std::mutex m;
-  return m;
-}
-
 int encode_q_map(CUtensorMap* map, const void* q, const gqa_problem& p, int qpt) {
   return encode_half_map(map, q, p.batch, p.heads_q, p.seq_q, p.head_dim, p.q_stride,
                          static_cast<uint32_t>(qpt),
@@ -432,7 +428,7 @@ GQA_API int gqa_forward(const gqa_problem* pp, const void* q, const void* k, con
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
     return GQA_ERR_LAYOUT;
 
-  const std::lock_guard<std::mutex> together(enqueue_mutex());
+  const EnqueueTurn turn(workspace);
   if (plan.kernel == GQA_KERNEL_DECODE) {
     const DecodeShape s = plan_decode(p, sms);
     CUtensorMap tmk, tmv;

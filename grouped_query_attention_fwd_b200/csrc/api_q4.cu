@@ -4,6 +4,7 @@
 
 #include <cstring>
 
+#include "enqueue_turn.h"
 #include "gqa.h"
 #include "kernels.h"
 #include "q4.cuh"
@@ -445,7 +446,7 @@ GQA_API int gqa_forward_q4(const gqa_problem* pp, const void* q, const void* cac
   if (!aligned(q, 16) || !aligned(cache_k, 16) || !aligned(cache_v, 16) || !aligned(out, 16))
     return GQA_ERR_LAYOUT;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const std::lock_guard<std::mutex> together(enqueue_mutex());
+  const EnqueueTurn turn(workspace);
   if (plan.kernel == GQA_KERNEL_Q4_PREFILL)
     return run_slices(p, plan_slices(p, sms), sms, q, static_cast<const uint8_t*>(cache_k),
                       static_cast<const uint8_t*>(cache_v), p.has_mask ? mask : nullptr, out, ws,

@@ -6,8 +6,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
 #include "gqa.h"
 
 namespace gqa {
@@ -308,10 +306,6 @@ ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count);
 int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs& a, uint8_t* ws,
                     const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                     cudaStream_t stream);
-// Held while a forward enqueues its launches: several of them may share scratch
-// in the workspace, so another thread's call on the same stream and workspace
-// must not come between them.
-std::mutex& enqueue_mutex();
 // Tensor map of Q tiles: boxes of qpt positions of the g heads of a kv head (api.cu).
 int encode_q_map(CUtensorMap* map, const void* q, const gqa_problem& p, int qpt);
 
