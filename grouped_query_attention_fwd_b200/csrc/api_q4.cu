@@ -263,9 +263,10 @@ int run_slices(const gqa_problem& p, const SlicePlan& s, int sms, const void* q,
       }
       a.vec = true;
       // The prefill uses nothing past a length, nor key tiles below the window
-      // of the first query.
+      // of the first query or past the diagonal of the last.
       a.leave_tail = true;
       a.from = p.window > 0 ? p.causal_offset - p.seq_k - p.window + 1 : -kLim;
+      a.to = p.causal ? p.causal_offset - p.seq_k + p.seq_q : 0;
       int rc = launch_q4_read(a, f16, stream);
       if (rc != GQA_OK) return rc;
       rc = launch_prefill_call(

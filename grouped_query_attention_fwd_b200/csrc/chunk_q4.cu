@@ -30,7 +30,9 @@
 // type, and fp16 (8 times finer) would not hold a bf16 cache's range: results
 // are 0.0036 off in bf16, against 0.0017 of rounding the result alone.  K's pairs are put in the dims' order (Q comes in it); V's stay as
 // the nibbles of a word fall (0 4 1 5 2 6 3 7), which permutes O's columns,
-// undone in registers at the end.  Values past a length are written as zeros.
+// undone in registers at the end.  Values of keys before the first or past the
+// last that a row of the group can see are written as zeros, whatever their
+// records hold.
 //
 // Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 180 us,
 // 760 TFLOP/s; a 128-key tile costs an SM about 2.6 us with two query tiles and
@@ -147,6 +149,7 @@ struct Share {
   Pair pr;               // mt0: the first query tile
   int id;                // group
   int nt_beg, nt_end;    // its key tiles that the query tiles can see
+  int key_beg, key_end;  // from the first key that one of their rows can see to past the last
   bool opens;            // the group's first unit is in this range
   int c_lo, c_hi;        // CTAs that share the group
 };
@@ -306,6 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       s.nt_beg = max(cu.kr.t0 + t0, static_cast<int>(lo / BN));
       s.nt_end = min(cu.kr.t0 + t1, static_cast<int>((hi + BN - 1) / BN));
       if (s.nt_end < s.nt_beg) s.nt_end = s.nt_beg;
+      s.key_beg = static_cast<int>(lo);
+      s.key_end = static_cast<int>(hi);
       s.opens = t0 == 0;
       s.c_lo = cta_of_unit(beg, sc.total, sc.P);
       s.c_hi = cta_of_unit(beg + cu.kr.tiles - 1, sc.total, sc.P);
@@ -493,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     each_share([&](const Share& me) {
       for (int nt = me.nt_beg; nt < me.nt_end; ++nt, ++U) {
-        const bool held = nt * BN + key < me.pr.len;
+        const bool held = nt * BN + key >= me.key_beg && nt * BN + key < me.key_end;
         const uint32_t buf = U & 1u;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {  // K, then V
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < G2; ++i)
-            if (!held) par[i] = 0u;  // past the length: zeros
+            if (!held) par[i] = 0u;  // seen by no row: zeros, whatever is there
           if (lane == 0) mbar_arrive(&raw_empty[s]);
           if (++s == R) {
             s = 0;

@@ -261,8 +261,8 @@ struct Q4RowsArgs {
   int64_t bt_stride, page_size, num_pages;
   bool vec;                 // every 16-bit row starts on 16 bytes
   bool leave_tail;          // read: rows past the length are left as they are, not zeroed
-  int64_t from;           // with leave_tail: rows below len + from (down to a whole 128-key
-                          // tile) are not written either
+  int64_t from, to;         // with leave_tail: only rows [len + from, len + to) are read, the
+                            // rest of the 128-key tiles they lie in is zeros up to the length
 };
 int launch_q4_append(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);

@@ -291,18 +291,24 @@ __global__ void __launch_bounds__(kThreads) gqa_q4_read_kernel(const Q4RowsArgs 
     uint16_t* dst = a.rows[kv] + b * rs[0] + h * rs[1] + d0;
     const int step = per_pass * kRows;
     const int64_t left = len - start;  // rows that exist, `held` of them asked for
-    const int held = left < 0 ? 0 : left < a.n ? static_cast<int>(left) : a.n;
-    const int n = a.leave_tail ? held : a.n;
-    int from = 0;
-    if (a.leave_tail && len + a.from > 0)
-      from = static_cast<int>(len + a.from < held ? len + a.from : held) / 128 * 128;
+    int held = left < 0 ? 0 : left < a.n ? static_cast<int>(left) : a.n;
+    int n = a.n, low = 0, from = 0;  // [low, held) are read, the rest of [from, n) is zeros
+    if (a.leave_tail) {
+      n = held;
+      if (len + a.to < held) {
+        held = len + a.to > 0 ? static_cast<int>(len + a.to) : 0;
+        n = min(n, (held + 127) / 128 * 128);
+      }
+      if (len + a.from > 0) low = len + a.from < held ? static_cast<int>(len + a.from) : held;
+      from = low / 128 * 128;
+    }
     for (int t0 = from + blockIdx.x * step; t0 < n; t0 += gridDim.x * step) {
       uint32_t par[kRows], word[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const int t = t0 + k * per_pass + slot;
         par[k] = word[k] = 0u;  // reads as zeros
-        if (t >= held) continue;
+        if (t < low || t >= held) continue;
         const int64_t at = record_at(a, kv, b, h, start + t);
         if (at < 0) {
           if (kv == 0 && h == 0 && d0 == 0) atomicOr(a.err, kErrPage);

@@ -381,7 +381,12 @@ GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const v
  * the 16-bit type, on the way to the tensor cores (GQA_KERNEL_Q4_CHUNK) or in
  * scratch (GQA_KERNEL_Q4_PREFILL; part of plan.workspace_bytes, at most 1 GiB
  * unless one head's keys alone need more).  What decides is the estimated time
- * of each.
+ * of each; a single token always takes the first.
+ * A key that no query of the block can see by lengths, diagonal and window
+ * never reaches the result, whatever its record holds.  One that some query
+ * sees, or that only the mask hides, stays out of the other rows with
+ * GQA_KERNEL_Q4; the longer blocks give it a weight of zero, which does not
+ * keep out an infinity or a NaN among its values.
  */
 GQA_API int gqa_query_q4(const gqa_problem* p, int sm_count, gqa_plan* plan);
 GQA_API int gqa_forward_q4(const gqa_problem* p, const void* q, const void* cache_k,

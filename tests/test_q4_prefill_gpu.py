@@ -210,3 +210,48 @@ def test_a_narrow_last_slice_keeps_its_keys(gqa):
             err = (out[b, :, i].double() - ref).abs()
             assert torch.all(err <= bound), (b, i, float((err / bound).max()))
             assert float(err.norm() / ref.norm()) <= 1e-2, (b, i)
+
+
+@pytest.mark.parametrize("Sq,window,page,masked,kernel", [
+    (1, 0, 0, False, "q4"), (3, 100, 64, False, "q4"),
+    (100, 0, 0, False, "q4_chunk"), (300, 0, 64, False, "q4_chunk"),
+    (300, 700, 0, False, "q4_chunk"), (220, 700, 128, False, "q4_chunk"),
+    (700, 0, 0, True, "q4_prefill"), (700, 0, 64, True, "q4_prefill"),
+    (701, 444, 0, True, "q4_prefill"),
+])
+def test_keys_that_no_query_sees_hold_anything(gqa, Sq, window, page, masked, kernel):
+    """A cache written up to a position, without lengths: NaN records past the
+    last query's diagonal, and below the first one's window, change nothing."""
+    B, Hq, Hkv, Sk, D, at = 3, 8, 2, 2944, 128, 1701
+    ck, _ = _records(gqa, B, Hkv, Sk, D, "bf16", 21, True)
+    cv, _ = _records(gqa, B, Hkv, Sk, D, "bf16", 22, False)
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    q = torch.randn(B, Hq, Sq, D, generator=gen, device="cuda").bfloat16()
+    kw = dict(causal=True, causal_offset=at - Sq, window=window)
+    if masked:
+        kw["mask"] = torch.rand(B, Sq, Sk, generator=gen, device="cuda") < 0.8
+    if page:
+        per = Sk // page
+        order = torch.randperm(B * per, generator=gen, device="cuda").view(B, per)
+        kw["block_table"] = order.int()
+
+    def call(k, v):
+        if page:
+            pools = []
+            for c in (k, v):
+                pool = torch.empty(B * per, Hkv, page, c.shape[-1], dtype=torch.uint8,
+                                   device="cuda")
+                pool[order] = c.unflatten(2, (per, page)).transpose(1, 2)
+                pools.append(pool)
+            k, v = pools
+        assert gqa.query_q4(q, k, v, **kw)["kernel_name"] == kernel
+        return gqa.forward_q4(q, k, v, **kw)
+
+    clean = call(ck, cv)
+    for c in (ck, cv):
+        c[:, :, at:] = 0xFF
+        if window:
+            c[:, :, :at - Sq + 1 - window] = 0xFF
+    dirty = call(ck, cv)
+    assert gqa.device_status() == gqa.GQA_OK
+    assert torch.all(torch.isfinite(clean)) and torch.equal(clean, dirty)
