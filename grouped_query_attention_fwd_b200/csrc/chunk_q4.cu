@@ -359,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int p1 = __shfl_sync(0xffffffffu, my_page, 2 * i + 1);
             for (int x = 0; x < 2; ++x) {  // K, then V
               if (!wait(&raw_empty[s], parity)) return false;
+              if (ca.withhold >= 0 && ca.withhold == me.id * ca.tiles + nt) return false;
               if (lane == 0) {
                 const CUtensorMap* map = x == 0 ? &tmk : &tmv;
                 uint8_t* dst = raw + s * L::kRaw;
@@ -940,6 +941,8 @@ int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs
   ca.info = reinterpret_cast<int2*>(ws + s.info_offset);
   ca.part_ml = reinterpret_cast<float2*>(ws + s.part_ml_offset);
   ca.part_o = reinterpret_cast<float*>(ws + s.part_o_offset);
+  uint64_t limit;  // (the kernel's waits keep theirs)
+  decode_test_settings(&ca.withhold, &limit);
   PagedKV pg{};
   pg.bt = p.block_table;
   pg.bt_stride = p.block_table_stride;

@@ -298,6 +298,7 @@ struct ChunkArgs {
   int2* info;         // per group: the opening CTA's partial slot, partials
   float2* part_ml;    // [slot][query tile][row]
   float* part_o;      // [slot][query tile][row][D]
+  int withhold;       // test only (gqa_debug_decode_withhold): key tile never issued, or -1
 };
 constexpr int kChunkThreads = 640;
 // Time of a key tile on an SM, with one query tile and with two.

@@ -413,14 +413,16 @@ GQA_API int gqa_debug_decode_trace(void* device_buffer, int64_t bytes);
 /*
  * gqa_debug_decode_withhold -- test of the kernels' bounded waits (failure
  * detection without a GPU fault; the pages have no counterpart).  The NEXT
- * decode launch of the process (gqa_forward or gqa_forward_decode_noalloc)
- * uses `wait_limit_ns` (1000 .. 1e9) as the limit of every internal wait and,
+ * decode launch of the process (gqa_forward, gqa_forward_decode_noalloc, or
+ * gqa_forward_q4 with GQA_KERNEL_Q4) uses `wait_limit_ns` (1000 .. 1e9) as the limit of every internal wait and,
  * if `unit` >= 0, its producer never issues the copies of that 128-key unit
  * (index in launch order) and issues nothing after it: the consumers' wait
  * for the unit runs out, the CTA unwinds (every copy already issued lands
  * first), the output is undefined and gqa_device_status then returns
  * GQA_ERR_TIMEOUT and re-zeroes the workspace.  The setting is consumed by
- * that one launch.  Returns GQA_OK or GQA_ERR_ARG.
+ * that one launch.  A launch of GQA_KERNEL_Q4_CHUNK takes it, too: the unit is
+ * then a key tile, counted on by the capacity's key tiles per group of query
+ * tiles, and the waits keep their limit of 1 s.  Returns GQA_OK or GQA_ERR_ARG.
  */
 GQA_API int gqa_debug_decode_withhold(int64_t unit, int64_t wait_limit_ns);
 

@@ -264,3 +264,91 @@ def test_same_bits_whoever_merges(gqa, B, Hq, Hkv, S, D, lens):
         outs.append(gqa.forward_q4(q, ck, cv, **kw))
     assert gqa.device_status() == gqa.GQA_OK
     assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("B,Hkv,Sq,S,D,unit", [
+    (4, 2, 512, 2048, 128, 0),      # two query tiles per group: 64 groups of 16 key tiles
+    (4, 2, 512, 2048, 128, 249),
+    (2, 2, 32, 8192, 64, 100),      # one query tile, split over CTAs
+])
+def test_chunk_wait_runs_out_and_is_reported(gqa, B, Hkv, Sq, S, D, unit):
+    """The chunk kernel without the copies of one key tile gives up its bounded
+    wait (1 s) and says so; the next call with the same workspace is right."""
+    ck, cv = _cache(gqa, B, Hkv, S, D)
+    q = _q(B, 4 * Hkv, Sq, D)
+    plan = gqa.query_q4(q, ck, cv)
+    assert plan["kernel_name"] == "q4_chunk" and unit < plan["work_units"]
+    want = _fresh(gqa, q, ck, cv, {})
+    ws = torch.zeros(plan["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    gqa.debug_decode_withhold(unit, 1_000_000)
+    gqa.forward_q4(q, ck, cv, workspace=ws)
+    assert gqa.device_status(ws) == gqa.GQA_ERR_TIMEOUT
+    out = gqa.forward_q4(q, ck, cv, workspace=ws)
+    assert gqa.device_status(ws) == gqa.GQA_OK
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("layout", ["heads", "pages"])
+@pytest.mark.parametrize("Sq,masked,kernel,dtype", [
+    (1, False, "q4", "bf16"), (5, True, "q4", "fp16"), (200, False, "q4_chunk", "bf16"),
+    (200, False, "q4_chunk", "fp16"), (600, True, "q4_prefill", "bf16"),
+])
+def test_attention_past_32_bits(gqa, Sq, masked, kernel, dtype, layout):
+    """Records past 4 GB of a cache's base, by the strides of its heads or by
+    their pages, each way, against 64 bits with the roundings of that way."""
+    n, D, H, g, page = 2048, 128, 2, 8, 64
+    if torch.cuda.mem_get_info()[0] < 14 << 30:
+        pytest.skip("needs 14 GB")
+    t, unit = (torch.bfloat16, 2.0 ** -8) if dtype == "bf16" else (torch.float16, 2.0 ** -11)
+    R, far, table = gqa.q4_record_bytes(D), (1 << 32) + (1 << 20), None
+    big = [torch.empty(far + n * 80 * 2 + (1 << 20), dtype=torch.uint8, device="cuda")
+           for _ in range(2)]
+    if layout == "heads":  # the second head starts past 4 GB
+        far = far // 16 * 16
+        caches = [c.as_strided((1, H, n, R), (far * H, far, R, 1)) for c in big]
+    else:
+        pages = big[0].numel() // (H * page * R)
+        caches = [c[:pages * H * page * R].view(pages, H, page, R) for c in big]
+        table = (pages - 1 - 2 * torch.arange(n // page, device="cuda")).int()[None]
+        assert (pages - 1 - n // page * 2) * H * page * R > (1 << 32) - (1 << 20)
+        assert (pages - 1) * H * page * R > 1 << 32
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = _q(1, H, n, D, t, seed=60), _q(1, H, n, D, t, seed=61)
+    gqa.kv_append_q4(caches[0], caches[1], k, v, lens, block_table=table)
+    q = _q(1, g * H, Sq, D, t, seed=62)
+    kw = dict(causal=True, causal_offset="bottom_right", block_table=table)
+    i = torch.arange(Sq, device="cuda")[:, None] + n - Sq
+    see = torch.arange(n, device="cuda")[None, :] <= i
+    if masked:
+        kw["mask"] = (torch.rand(1, Sq, n, device="cuda",
+                                 generator=torch.Generator(device="cuda").manual_seed(63)) < 0.7)
+        see &= kw["mask"][0]
+    assert gqa.query_q4(q, *caches, **kw)["kernel_name"] == kernel
+    out = gqa.forward_q4(q, *caches, **kw).double()[0]
+    assert gqa.device_status() == gqa.GQA_OK
+    for h in range(H):
+        # The records' values, in 64 bits.
+        vals = []
+        for c in caches:
+            rec = c[0, h] if table is None else c[table[0].long()][:, h].reshape(n, R)
+            par = rec[:, :16].contiguous().view(t).double().view(n, 4, 2)
+            code = torch.stack([rec[:, 16:] % 16, rec[:, 16:] // 16], -1).double().view(n, 4, 32)
+            vals.append((code * par[..., :1] + par[..., 1:]).flatten(-2))
+        kk, vv = vals
+        scale_v = par[..., 0].repeat_interleave(32, -1)
+        for x in range(g):
+            qh = q[0, h * g + x].double()
+            p = torch.softmax((qh @ kk.T / D ** 0.5).masked_fill(~see, -torch.inf), -1)
+            ref = p @ vv
+            bound = 1.01 * unit * ref.abs() + 2.0 ** -14 * (p @ vv.abs()) + 2.0 ** -24
+            if kernel == "q4":  # the weights, once to fp16, times codes of at most 15 scales
+                bound += 2.0 ** -11 * 15 * (p @ scale_v)
+            else:               # keys, values and weights, once to the type
+                move = 2.1 * unit / D ** 0.5 * (qh.abs() @ kk.abs().T).amax(-1, keepdim=True)
+                bound += (p @ vv.abs()) * (2.02 * unit + move)
+            err = (out[h * g + x] - ref).abs()
+            assert torch.all(err <= bound), float((err / bound).max())
+            # Most roundings fall on both sides of half of their bound: in norm,
+            # the result's alone stays within it, with three more within twice.
+            assert float(err.norm() / ref.norm()) <= unit * (1 if kernel == "q4" else 2)
