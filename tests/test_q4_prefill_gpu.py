@@ -255,3 +255,45 @@ def test_keys_that_no_query_sees_hold_anything(gqa, Sq, window, page, masked, ke
     dirty = call(ck, cv)
     assert gqa.device_status() == gqa.GQA_OK
     assert torch.all(torch.isfinite(clean)) and torch.equal(clean, dirty)
+
+
+@pytest.mark.parametrize("scale", [0.02, 0.3, 0.0, -0.11, -1.0])
+@pytest.mark.parametrize("Sq,masked,causal,dtype,kernel", [
+    (1, False, False, "bf16", "q4"), (3, True, True, "fp16", "q4"), (2, False, True, "bf16", "q4"),
+    (40, False, False, "bf16", "q4_chunk"), (300, False, False, "fp16", "q4_chunk"),
+    (300, False, True, "bf16", "q4_chunk"), (700, True, False, "bf16", "q4_prefill"),
+])
+def test_scales_and_blocks_without_a_diagonal(gqa, Sq, masked, causal, dtype, kernel, scale):
+    """Scales other than 1 / sqrt(D), zero and negative ones among them, and
+    long blocks whose queries see every key of their sequence."""
+    B, Hq, Hkv, Sk, D = 2, 16, 2, 3700, 128
+    ck, k64 = _records(gqa, B, Hkv, Sk, D, dtype, 31, True)
+    cv, v64 = _records(gqa, B, Hkv, Sk, D, dtype, 32, False)
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    q = torch.randn(B, Hq, Sq, D, generator=gen, device="cuda").to(u.TORCH[dtype])
+    lens = torch.tensor([Sk, 2900], dtype=torch.int32, device="cuda")
+    kw = dict(scale=scale, kv_lens=lens)
+    if causal:
+        kw.update(causal=True, causal_offset="bottom_right")
+    if masked:
+        kw["mask"] = torch.rand(B, Sq, Sk, generator=gen, device="cuda") < 0.7
+    assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == kernel
+    out = gqa.forward_q4(q, ck, cv, **kw)
+    assert gqa.device_status() == gqa.GQA_OK
+    g, unit = Hq // Hkv, u.UNIT[dtype]
+    for b, n in enumerate(lens.tolist()):
+        see = torch.ones(Sq, n, dtype=torch.bool, device="cuda")
+        if causal:
+            see = torch.arange(n, device="cuda") <= torch.arange(Sq, device="cuda")[:, None] + n - Sq
+        if masked:
+            see = see & kw["mask"][b, :, :n]
+        for h in range(Hq):
+            k, v, qh = k64[b, h // g, :n], v64[b, h // g, :n], q[b, h].double()
+            p = torch.softmax((qh @ k.T * scale).masked_fill(~see, -math.inf), -1)
+            ref = p @ v
+            # The roundings of test_long_query_blocks; fewer in the short blocks.
+            move = 2.1 * abs(scale) * unit * (qh.abs() @ k.abs().T).amax(-1, keepdim=True)
+            bound = (p @ v.abs()) * (2.02 * unit + move + 2.0 ** -14) + \
+                1.01 * unit * ref.abs() + 2.0 ** -24
+            err = (out[b, h].double() - ref).abs()
+            assert torch.all(err <= bound), float((err / bound).max())
