@@ -14,13 +14,15 @@ namespace {
 
 constexpr int64_t kLim = int64_t(1) << 31;
 
-// Times that the choice between the two ways of attending goes by (ns, this
-// library's kernels): launch and ends of a decode; a slice's launches and ends,
-// a key tile of the two-tile prefill; bytes read and written by the read back.
-constexpr double kDecodeNs = 10000;
-constexpr double kSliceNs = 12000, kTwoTileNs = 2200, kReadBytesPerNs = 4500;
-// Launches and ends of the 128-row kernel, and a key tile of one of its SMs.
-constexpr double kChunkNs = 20000;
+// Times that the choice between the three ways of attending goes by (ns, this
+// library's kernels; with those per unit and key tile in kernels.h): launch and
+// ends of a decode; launches and ends of the 128-row kernel, and each partial
+// of a group that its merge reads; a slice's launches and ends, a key tile of
+// the two-tile prefill, and bytes per ns of the read back.
+constexpr double kDecodeNs = 7000;
+constexpr double kChunkNs = 16000, kChunkPartialNs = 300;
+constexpr double kSliceNs = 9000, kReadBytesPerNs = 4500;
+double two_tile_ns(int64_t head_dim) { return head_dim > 64 ? 2000 : 1700; }
 
 bool aligned(const void* ptr, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(ptr) & (a - 1)) == 0;
@@ -137,36 +139,49 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
   const double bytes = 2.0 * double(p.batch * p.heads_kv) *
                        double(keys * (q4::record_bytes(static_cast<int>(p.head_dim)) +
                                          2 * p.head_dim));
-  s.ns = double(s.slices) * (kSliceNs + rounds * double((keys + 127) / 128) * kTwoTileNs) +
+  s.ns = double(s.slices) * (kSliceNs + rounds * double((keys + 127) / 128) * two_tile_ns(p.head_dim)) +
          bytes / kReadBytesPerNs;
   return s;
 }
 
 // Estimated times of the other two ways over the same problem.
 double decode_ns(const gqa_problem& p, const DecodeShape& s, int sms) {
-  const double units = double(s.groups) * double((keys_read(p) + 127) / 128);
-  return kDecodeNs + units / sms * kQ4UnitNs;
+  const double tiles = double((keys_read(p) + 127) / 128);
+  const double places = s.split > 0 ? tiles / s.split : double(s.groups) * (tiles + s.lead) / sms;
+  return kDecodeNs + places * q4_unit_ns(s.D) + (s.split == 1 ? 0.0 : kQ4MergeNs);
 }
 
 double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
-  const double places = double(s.groups) * double((keys_read(p) + 127) / 128 + kChunkLead);
-  return kChunkNs + places / sms * (s.nq == 2 ? kChunkPairNs : kChunkTileNs);
+  const double tiles = double((keys_read(p) + 127) / 128), share = double(sms) / double(s.groups);
+  return kChunkNs + double(s.groups) * (tiles + kChunkLead) / sms * chunk_tile_ns(s.D, s.nq) +
+         kChunkPartialNs * (share < tiles ? share : tiles);
 }
 
 // The way to attend: a pass over the records per 8 rows of a kv head (one pass
 // where it has no more), 128-row tiles that unpack each record once, or the
-// two-tile prefill over 16-bit scratch.  The last two are planned, and their
-// plans filled in, only where the first is not taken outright: the tiles of a
-// single token of more than 128 query heads per kv head would hold no query
+// two-tile prefill over 16-bit scratch: the least of the estimated times.  Over
+// 468 problems (1024 to 16384 keys, 2 to 128 kv heads, 4 and 8 query heads
+// each, 3 to 1024 queries, head dims 64 and 128), each timed with every way, it
+// takes 0.4% longer than the fastest in the mean and 12% at most.
+//
+// With per-sequence lengths a slice takes as long as its longest sequence, the
+// other two as all of them together: counted as three quarters of the most.
+//
+// A single token always takes the first, however many query heads share a kv
+// head.  At 32 of them that takes 2.7 us per 128 keys of a kv head and SM
+// against 2.1 us in 128-row tiles, at 64 5.2 us.  The last two ways are
+// planned, and their plans filled in, only where there is a choice: the tiles
+// of a token of more than 128 query heads per kv head would hold no query
 // position.
 int pick_way(const gqa_problem& p, const DecodeShape& d, int sms, ChunkShape* c, SlicePlan* s) {
   if (d.passes <= 1 || p.seq_q <= 1) return GQA_KERNEL_Q4;
   *c = plan_chunk_q4(p, sms);
   *s = plan_slices(p, sms);
-  double best = decode_ns(p, d, sms);
+  const double held = p.kv_lens != nullptr ? 0.75 : 1.0;
+  double best = held * decode_ns(p, d, sms);
   int way = GQA_KERNEL_Q4;
-  if (c->fits && chunk_ns(p, *c, sms) < best) {
-    best = chunk_ns(p, *c, sms);
+  if (c->fits && held * chunk_ns(p, *c, sms) < best) {
+    best = held * chunk_ns(p, *c, sms);
     way = GQA_KERNEL_Q4_CHUNK;
   }
   return s->ns < best ? GQA_KERNEL_Q4_PREFILL : way;

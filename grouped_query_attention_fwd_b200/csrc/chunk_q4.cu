@@ -898,9 +898,9 @@ ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count) {
                 : decode_key_range(p.seq_k, p.seq_k, p.seq_q, p.causal, p.causal_offset, p.window)
                       .tiles;
   if (s.tiles < 1) s.tiles = 1;
-  // A pair of query tiles costs kChunkPairNs a key tile and one alone
-  // kChunkTileNs: two at a time are cheaper as soon as there are two, even
-  // where the last pair is half empty.
+  // A pair of query tiles costs less than two alone (chunk_tile_ns): two at a
+  // time are cheaper as soon as there are two, even where the last pair is half
+  // empty.
   s.nq = s.m_tiles > 1 ? 2 : 1;
   s.m_groups = (s.m_tiles + s.nq - 1) / s.nq;
   s.groups = p.batch * p.heads_kv * s.m_groups;

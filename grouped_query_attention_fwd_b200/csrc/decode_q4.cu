@@ -1322,8 +1322,8 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
   const int64_t rows = p.heads_q / p.heads_kv * p.seq_q;
   s.D = p.head_dim <= 64 ? 64 : 128;
   // One column tile per pass: two would serve 16 rows with one unpacking, but
-  // leave too few registers for 64-key chunks (1790 ns per unit against twice
-  // 550; the passes' records come out of L2 the second time).
+  // leave registers for one 16-key MMA tile at a time only (1790 ns per unit
+  // against twice 640; the passes' records come out of L2 the second time).
   s.NT = 1;
   s.HP = 8;
   s.passes = static_cast<int>((rows + s.HP - 1) / s.HP);
@@ -1345,9 +1345,9 @@ DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count) {
   if (!s.ragged && s.groups > 0 && s.groups <= sm_count) {
     int64_t split = sm_count / s.groups;
     if (split > s.tiles_per_group) split = s.tiles_per_group;
-    const double apart = double((s.tiles_per_group + split - 1) / split) * kQ4UnitNs +
+    const double apart = double((s.tiles_per_group + split - 1) / split) * q4_unit_ns(s.D) +
                          (split > 1 ? kQ4MergeNs : 0.0);
-    const double even = double((s.units + sm_count - 1) / sm_count) * kQ4UnitNs + kQ4MergeNs;
+    const double even = double((s.units + sm_count - 1) / sm_count) * q4_unit_ns(s.D) + kQ4MergeNs;
     if (apart <= even) {
       s.split = static_cast<int>(split);
       s.lead = 0;

@@ -270,11 +270,12 @@ int launch_q4_read(const Q4RowsArgs& a, bool f16, cudaStream_t stream);
 // Attention over records for single tokens and short query blocks: the shape,
 // arguments (make_decode_args) and workspace of the 16-bit decode.
 DecodeShape plan_decode_q4(const gqa_problem& p, int sm_count);
-// Measured times that plans go by (ns): a 128-key unit of one SM, the merge of
-// a split group's partials; and what a change of groups inside a range costs,
-// in units.
-constexpr double kQ4UnitNs = 550, kQ4MergeNs = 2500;
-constexpr int kQ4Lead = 8, kChunkLead = 6;
+// Measured times that plans go by (ns): a 128-key unit of one SM at head dims
+// padded to D, the merge of a split group's partials; and what a change of
+// groups inside a range costs, in units.
+inline double q4_unit_ns(int D) { return D == 128 ? 640 : 430; }
+constexpr double kQ4MergeNs = 2500;
+constexpr int kQ4Lead = 10;
 constexpr int kQ4Threads = 384;
 int launch_decode_q4(const gqa_problem& p, const DecodeShape& s, const DecodeArgs& a, uint8_t* ws,
                      const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream);
@@ -301,8 +302,12 @@ struct ChunkArgs {
   int withhold;       // test only (gqa_debug_decode_withhold): key tile never issued, or -1
 };
 constexpr int kChunkThreads = 640;
-// Time of a key tile on an SM, with one query tile and with two.
-constexpr int kChunkTileNs = 1950, kChunkPairNs = 2600;
+// Measured time of a key tile on an SM (ns), with nq query tiles; and what a
+// change of groups costs, in key tiles.
+inline double chunk_tile_ns(int D, int nq) {
+  return D == 128 ? (nq == 2 ? 2750 : 1820) : (nq == 2 ? 2070 : 1190);
+}
+constexpr int kChunkLead = 6;
 ChunkShape plan_chunk_q4(const gqa_problem& p, int sm_count);
 int launch_chunk_q4(const gqa_problem& p, const ChunkShape& s, const PrefillArgs& a, uint8_t* ws,
                     const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,

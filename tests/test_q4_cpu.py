@@ -265,3 +265,20 @@ def test_no_non_coherent_loads():
     for path in sources:
         text = open(path).read()
         assert not re.search(r"__ldg\s*\(|\.nc\.|__restrict__", text), path
+
+
+@pytest.mark.parametrize("B,Hkv,g,Sq,Sk,D,way,times", [
+    # Measured with each way, us: decode, 128-row tiles, slices.  Many short
+    # groups: their changes cost a decode more than their units.
+    (16, 8, 8, 8, 1024, 128, "q4_chunk", (96, 38, 45)),
+    (16, 8, 8, 6, 1024, 64, "q4_chunk", (49, 29, 31)),
+    (2, 8, 8, 24, 1024, 128, "q4_chunk", (46, 26, 29)),
+    # Few groups, long keys: the tiles' partials cost more than unpacking again.
+    (1, 2, 8, 16, 16384, 64, "q4", (23, 45, 215)),
+    (1, 2, 4, 32, 16384, 128, "q4", (30, 49, 256)),
+    (16, 8, 4, 1024, 16384, 128, "q4_prefill", (None, 5013, 4887)),
+])
+def test_the_way_follows_measured_times(gqa, B, Hkv, g, Sq, Sk, D, way, times):
+    p = _problem(gqa, B, Hkv * g, Hkv, Sq, Sk, D, causal=True)
+    p.causal_offset = Sk - Sq
+    assert gqa.KERNEL_NAMES[_rc(gqa, p)[1].kernel] == way

@@ -269,7 +269,7 @@ def test_same_bits_whoever_merges(gqa, B, Hq, Hkv, S, D, lens):
 @pytest.mark.parametrize("B,Hkv,Sq,S,D,unit", [
     (4, 2, 512, 2048, 128, 0),      # two query tiles per group: 64 groups of 16 key tiles
     (4, 2, 512, 2048, 128, 249),
-    (2, 2, 32, 8192, 64, 100),      # one query tile, split over CTAs
+    (2, 8, 32, 8192, 64, 700),      # one query tile, split over CTAs
 ])
 def test_chunk_wait_runs_out_and_is_reported(gqa, B, Hkv, Sq, S, D, unit):
     """The chunk kernel without the copies of one key tile gives up its bounded
