@@ -79,6 +79,13 @@ static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIoRegs <= 5 * kLaunchRegs, "re
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // S_X at 128 X, O_X at kOCol + 128 X
 
+// P is taken 2^kWeightLog2 times as large, as far as the reference that trails
+// by 2^kRescaleLog2 lets fp16: weights keep 11 bits down to 2^-21 of the
+// largest, and 8 down to 2^-24 (a row may leave most of its weight on a key
+// whose values are zeros).
+constexpr float kWeightLog2 = 7.f;
+static_assert(kWeightLog2 + kRescaleLog2 < 16.f, "P stays in fp16");
+
 template <int D>
 struct ChunkLayout {
   static constexpr int NG = D / kGroup;
@@ -645,7 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float ref = exp_ref(m_ref);
           const float sc = fast ? a.scale_log2 : 1.f;
-          const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(-ref, -ref);
+          const float up = kWeightLog2 - ref;
+          const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(up, up);
           uint64_t lp[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) lp[e] = 0;

@@ -297,3 +297,53 @@ def test_scales_and_blocks_without_a_diagonal(gqa, Sq, masked, causal, dtype, ke
                 1.01 * unit * ref.abs() + 2.0 ** -24
             err = (out[b, h].double() - ref).abs()
             assert torch.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("dtype", ["fp16"])
+@pytest.mark.parametrize("share", [2.0 ** -6, 2.0 ** -14])
+def test_weight_on_a_key_of_zeros(gqa, dtype, share):
+    """Nearly all weight on one key whose values are zeros, as heads that have
+    nothing to add put it: what the other keys add, `share` of the weight over
+    2000 keys, keeps its bits."""
+    B, Hq, Hkv, Sq, Sk, D = 1, 8, 2, 512, 2048, 128
+    gen = torch.Generator(device="cuda").manual_seed(51)
+    t = u.TORCH[dtype]
+    k, v = (torch.randn(B, Hkv, Sk, D, generator=gen, device="cuda") for _ in range(2))
+    q = torch.randn(B, Hq, Sq, D, generator=gen, device="cuda") * 0.1
+    k[:, :, 0], q[..., 0] = 0, 1.0
+    k[..., 0] = 0
+    # Score of key 0 above the others', whose weights are about equal.
+    k[:, :, 0, 0] = math.sqrt(D) * (math.log(Sk) - math.log(share))
+    v[:, :, 0] = 0
+    k, v, q = k.to(t), v.to(t), q.to(t)
+    ck = torch.zeros(B, Hkv, Sk, u.record_bytes(D), dtype=torch.uint8, device="cuda")
+    cv = torch.zeros_like(ck)
+    gqa.kv_append_q4(ck, cv, k, v, torch.zeros(B, dtype=torch.int32, device="cuda"))
+    k64, v64 = [], []
+    for c, out in ((ck, k64), (cv, v64)):
+        par = c[..., :16].contiguous().view(t).double().unflatten(-1, (4, 2))
+        code = torch.stack([c[..., 16:] % 16, c[..., 16:] // 16], -1).double().flatten(-2)
+        out.append((code.unflatten(-1, (4, 32)) * par[..., :1] + par[..., 1:]).flatten(-2))
+    k64, v64 = k64[0], v64[0]
+    kw = dict(causal=True, causal_offset="bottom_right")
+    assert gqa.query_q4(q, ck, cv, **kw)["kernel_name"] == "q4_chunk"
+    out = gqa.forward_q4(q, ck, cv, **kw).double()
+    assert gqa.device_status() == gqa.GQA_OK
+    see = torch.arange(Sk, device="cuda") <= torch.arange(Sq, device="cuda")[:, None] + Sk - Sq
+    for h in range(Hq):
+        kk, vv, qh = k64[0, h // 4], v64[0, h // 4], q[0, h].double()
+        p = torch.softmax((qh @ kk.T / math.sqrt(D)).masked_fill(~see, -math.inf), -1)
+        assert float(p[:, 0].min()) > 0.5 and not vv[0].any()
+        ref = p @ vv
+        # The one key's score, off by half a step of fp16, moves all other weights
+        # alike: `fit`.  Beside that, keys and values rounded to fp16's 2^-11,
+        # weights to that or 2^-32 of the largest, the result to its type (fp16's
+        # subnormal step: 2^-25).
+        moves = qh.abs() @ kk.abs().T / math.sqrt(D)
+        fit = (out[0, h] * ref).sum(-1, keepdim=True) / (ref * ref).sum(-1, keepdim=True)
+        assert torch.all((fit - 1).abs() <= 2.1 * 2.0 ** -11 * moves[:, :1] + 2.0 ** -6)
+        move = moves[:, 1:].amax(-1, keepdim=True)
+        bound = (p @ vv.abs()) * (2.02 * 2.0 ** -11 + 2.1 * 2.0 ** -11 * move + 2.0 ** -14) + \
+            2.0 ** -32 * vv.abs().sum(0) + 1.01 * u.UNIT[dtype] * ref.abs() + 2.0 ** -25
+        err = (out[0, h] - fit * ref).abs()
+        assert torch.all(err <= bound), float((err / bound).max())
