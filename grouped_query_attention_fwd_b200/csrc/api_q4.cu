@@ -164,6 +164,9 @@ double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
 // each, 3 to 1024 queries, head dims 64 and 128), each timed with every way, it
 // takes 0.4% longer than the fastest in the mean and 12% at most.
 //
+// A bf16 slice, in which keys, values and weights are rounded to bf16, has to
+// save a tenth against the tiles, which keep fp16's bits of them.
+//
 // With per-sequence lengths a slice takes as long as its longest sequence, the
 // other two as all of them together: counted as three quarters of the most.
 //
@@ -184,7 +187,8 @@ int pick_way(const gqa_problem& p, const DecodeShape& d, int sms, ChunkShape* c,
     best = held * chunk_ns(p, *c, sms);
     way = GQA_KERNEL_Q4_CHUNK;
   }
-  return s->ns < best ? GQA_KERNEL_Q4_PREFILL : way;
+  const double bits = way == GQA_KERNEL_Q4_CHUNK && p.dtype == GQA_DTYPE_BF16 ? 1.1 : 1.0;
+  return bits * s->ns < best ? GQA_KERNEL_Q4_PREFILL : way;
 }
 
 int fill_plan_q4(const gqa_problem& p, int sm_count, gqa_plan* plan) {

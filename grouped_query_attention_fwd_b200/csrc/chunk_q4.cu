@@ -23,25 +23,32 @@
 // 2) may overwrite P(i), and the commit that signals S(i + 2) also means that
 // PV(i) is done and O_X may be rescaled.
 //
-// Unpacking: a pair of codes becomes 128 + c (bf16) or 1024 + c (fp16) by one
-// AND-OR, c by one packed subtraction, and the rounded value scale * c + min by
-// one packed fused multiply-add: one rounding to 16 bits per key and value
-// element, and P is rounded likewise.  The products take operands of one 16-bit
-// type, and fp16 (8 times finer) would not hold a bf16 cache's range: results
-// are 0.0036 off in bf16, against 0.0017 of rounding the result alone.  K's pairs are put in the dims' order (Q comes in it); V's stay as
-// the nibbles of a word fall (0 4 1 5 2 6 3 7), which permutes O's columns,
-// undone in registers at the end.  Values of keys before the first or past the
-// last that a row of the group can see are written as zeros, whatever their
-// records hold.
+// Unpacking: a pair of codes becomes 1024 + c (fp16) by one AND-OR, c by one
+// packed subtraction, and the rounded value scale * c + min by one packed fused
+// multiply-add: one rounding to 16 bits per key and value element, and P is
+// rounded likewise.  K's pairs are put in the dims' order (Q comes in it); V's
+// stay as the nibbles of a word fall (0 4 1 5 2 6 3 7), which permutes O's
+// columns, undone in registers at the end.  Values of keys before the first or
+// past the last that a row of the group can see are written as zeros, whatever
+// their records hold.
 //
-// Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 180 us,
-// 760 TFLOP/s; a 128-key tile costs an SM about 2.6 us with two query tiles and
-// 1.95 us with one, of which the products need 1.1 us and 0.55 us.  Bound: the
-// unpacking warps and the softmax, which share the issue slots.  With four
-// unpacking warps of twice the work each it took 197 us (164 us without their
-// arithmetic and stores, 154 us without the softmax, 145 us without either).  A
-// whole S row per thread costs some spills at 168 registers; fewer cost more
-// (152: 189 us, 136: 249 us).
+// Operands: the products take two operands of one 16-bit type.  A bf16 cache is
+// unpacked into fp16, which keeps 8 times as many bits (relative error against 64
+// bits 0.0017, the result's own rounding, against 0.0037 with bf16 operands and
+// P), its Q is brought to fp16 a share at a time, and P is fp16.  fp16 does not
+// hold bf16's range: a CTA that meets records or queries past what would keep
+// bf16's bits (see kUp) goes over its shares once more with bf16 operands, which
+// costs the others a barrier and a flag.  An fp16 cache's values are rounded to
+// fp16: 0.0005 against 0.0002.
+//
+// Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 186 us,
+// 735 TFLOP/s; with more keys a 128-key tile costs an SM 2.4 us with two query
+// tiles and 1.8 us with one (fp16 caches 2.3 and 1.6 us), of which the products
+// need 1.1 us and 0.55 us.  Bound: the unpacking warps and the softmax, which
+// share the issue slots.  With four unpacking warps of twice the work each it
+// took a tenth longer (a tenth less without their arithmetic and stores, a
+// sixth less without the softmax).  A whole S row per thread costs some spills
+// at 168 registers; fewer cost more (152: 5% longer, 136: 38%).
 //
 // Warp roles (640 threads, one CTA per SM):
 //   warps 0-3   softmax of X = 0 and its epilogue (thread t: row t)
@@ -49,6 +56,7 @@
 //   warps 8-15  unpacking (thread: one key, half of the dims)
 //   warp 16     TMA producer of Q tiles and records
 //   warp 17     TMEM allocator and MMA issuer (warps 18, 19 idle)
+// The softmax warps also bring a bf16 cache's Q to fp16.
 // Every wait is bounded; a thread that gives up sets the abort flag and the
 // error word, and every role leaves its loops.
 #include <cuda_runtime.h>
@@ -79,12 +87,35 @@ static_assert(2 * kSoftmaxRegs + 2 * kConvRegs + kIoRegs <= 5 * kLaunchRegs, "re
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kOCol = 256;  // S_X at 128 X, O_X at kOCol + 128 X
 
+// bf16 records in fp16 operands: values are taken kUp times as large, which puts
+// the middle of what fp16 holds where caches have their values.  They overflow
+// from scales of 2^7 or minima of 2^11 on (patterns in bf16).  A value's, scale's
+// and minimum's rounding is off by 2^-25 / kUp or 2^-12 of it: fewer bits than
+// bf16's where a group of V's is below 2^-16 throughout (eight scales and the
+// minimum are; groups of zeros may be), and, in the scores, where a row's
+// |scale * q| passes 2^9.
 // P is taken 2^kWeightLog2 times as large, as far as the reference that trails
 // by 2^kRescaleLog2 lets fp16: weights keep 11 bits down to 2^-21 of the
 // largest, and 8 down to 2^-24 (a row may leave most of its weight on a key
-// whose values are zeros).
+// whose values are zeros).  With bf16 operands, too: partials of a group meet.
 constexpr float kWeightLog2 = 7.f;
 static_assert(kWeightLog2 + kRescaleLog2 < 16.f, "P stays in fp16");
+constexpr float kUp = 16.f;
+constexpr uint32_t kUp2 = 0x41804180u;  // twice, in bf16
+constexpr uint32_t kMostScale = (127 + 7) << 7, kMostMin = (127 + 11) << 7;
+constexpr uint32_t kLeast = ((127 - 16 + 4) << 23) - 1;  // (kUp times the value's bits, less one)
+constexpr float kMostToLog2 = 0x1p9f / (0x1p15f * kUp);
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;  // (of a NaN and a number, the number: fp16 has NaN, too)
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
 
 template <int D>
 struct ChunkLayout {
@@ -99,7 +130,7 @@ struct ChunkLayout {
   __host__ __device__ static constexpr int v_off(int nq) { return (nq + 2) * kTile; }
   __host__ __device__ static constexpr int raw_off(int nq) { return (nq + 4) * kTile; }
   static int bytes(int nq, int stages, int ragged_batch) {
-    return 1024 + raw_off(nq) + stages * kRaw + (2 * stages + 18) * 8 + 16 +
+    return 1024 + raw_off(nq) + stages * kRaw + (2 * stages + 19) * 8 + 16 +
            (nq == 1 ? 2 * 2 * 128 * 8 : 0) +
            (ragged_batch > 0 ? ((8 * ragged_batch + 4 + 15) / 16) * 16 : 0);
   }
@@ -187,10 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* o_final = p_full + 2;    // the share's last PV done
   uint64_t* o_free = o_final + 1;    // both O_X read by the epilogue (8 warps)
   uint64_t* mma_done = o_free + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint64_t* q_ready = mma_done + 1;  // W: the share's Q in fp16 (8 warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_ready + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* redo = abort_flag + 1;  // fp16 operands would not do
   // With one query tile: [share & 1][X][row] (m, l), which a row's threads trade.
-  float2* xch = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(q_full) + 18 * 8 + 16);
+  float2* xch = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(q_full) + 19 * 8 + 16);
   int* len_s = reinterpret_cast<int*>(xch + (nq == 1 ? 512 : 0));
   int* pre_s = len_s + a.B;
 
@@ -199,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool ragged = a.lens != nullptr;
   const int gpb = a.Hkv * ca.m_groups;
 
-  if (threadIdx.x == 0) {
+  auto init_barriers = [&] {
     for (int i = 0; i < R; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], kConvWarps);
@@ -217,8 +250,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(o_final, 1);
     mbar_init(o_free, kSoftmaxWarps);
     mbar_init(mma_done, 1);
-    *abort_flag = 0;
+    mbar_init(q_ready, kSoftmaxWarps);
     fence_mbar_init();
+  };
+  if (threadIdx.x == 0) {
+    init_barriers();
+    *abort_flag = 0;
+    *redo = 0;
   }
   // Q rows past qpt * g of a tile are never written by TMA: zero them once.
   for (int i = threadIdx.x; i < nq * CH * (BM - ca.rows) * 8; i += kThreads) {
@@ -325,9 +363,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  // Each role's work, as body(whether the operands are fp16): over all shares
+  // with fp16 operands, and, where some of a bf16 cache's values turned out not
+  // to fit, over all of them once more with bf16 ones.
+  auto passes = [&](auto&& body) {
+    body(BoolConst<true>{});
+    if (F16) return;
+    tc_fence_before();
+    __syncthreads();  // every copy has landed, every product is done
+    tc_fence_after();
+    if (*redo == 0 || *abort_flag) return;
+    if (threadIdx.x == 0) {
+      for (uint64_t* b = raw_full; b <= q_ready; ++b) mbar_inval(b);
+      init_barriers();
+    }
+    __syncthreads();
+    body(BoolConst<false>{});
+  };
+
   if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIoRegs));
-    if (warp == kWarpLoad) {
+    if (warp == kWarpLoad) passes([&](auto) {
       // ------------------------------------------------------------ producer
       if (lane == 0) {
         prefetch_tmap(&tmq);
@@ -409,11 +465,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait_drain(&raw_full[j % R], (j / R) & 1u);
         if (n_share > 0) mbar_wait_drain(q_full, (n_share - 1) & 1u);
       }
-    } else if (warp == kWarpMMA) {
+    });
+    else if (warp == kWarpMMA) passes([&](auto half) {
       // ------------------------------------------------------------ MMA warp
       // Converged, one elected lane issues.
-      constexpr uint32_t idesc_qk = F16 ? idesc_f16_f32(BM, BN, 0, 0) : idesc_bf16_f32(BM, BN, 0, 0);
-      constexpr uint32_t idesc_pv = F16 ? idesc_f16_f32(BM, D, 0, 1) : idesc_bf16_f32(BM, D, 0, 1);
+      constexpr bool H = decltype(half)::value, W = H && !F16;
+      constexpr uint32_t idesc_qk = H ? idesc_f16_f32(BM, BN, 0, 0) : idesc_bf16_f32(BM, BN, 0, 0);
+      constexpr uint32_t idesc_pv = H ? idesc_f16_f32(BM, D, 0, 1) : idesc_bf16_f32(BM, D, 0, 1);
       const uint64_t dq0 = kmajor_desc(smem_u32(smem));
       const uint64_t dk0 = kmajor_desc(smem_u32(smem + L::k_off(nq)));
       const uint64_t dv0 = mnmajor_desc(smem_u32(smem + L::v_off(nq)), L::kChunkBytes);
@@ -468,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       each_share([&](const Share& me) {
         const int n = (me.nt_end - me.nt_beg) << sh;
         if (n == 0) return true;
-        if (!wait(q_full, n_share & 1u)) return false;
+        if (!wait(W ? q_ready : q_full, n_share & 1u)) return false;
         tc_fence_after();
         for (int i = 0; i < 2 && i < n; ++i)
           if (!issue_qk(i, i == n - 1)) return false;
@@ -483,311 +541,378 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) tc_commit(mma_done);
       __syncwarp();
       mbar_wait_drain(mma_done, 0);
-    }
+    });
+    else passes([](auto) {});
   } else if (warp >= 8) {
     // -------------------------------------------------------------- unpacking
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-    // A thread takes one key and half of the dims: NG / 2 groups.  Eight consecutive keys in a quarter-warp:
-    // neither the records' 16 (D / 32 + 1)-byte rows nor the swizzled 16-byte
-    // stores conflict.
-    constexpr int G2 = NG / 2;
-    const int key = static_cast<int>(threadIdx.x) & 127;
-    const int half = static_cast<int>(threadIdx.x - 256) >> 7;
-    const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
-    const uint32_t raw_at = smem_u32(raw) + key * P;
-    const uint32_t row_at = smem_u32(smem) + (CH == 2 ? half * L::kChunkBytes : half * 64) + key * 128;
-    const uint32_t k_at = row_at + L::k_off(nq), v_at = row_at + L::v_off(nq);
-    uint32_t U = 0;  // key tiles unpacked
-    int s = 0;
-    uint32_t parity = 0;
-    auto wait = [&](uint64_t* bar, uint32_t par) {
-      return __all_sync(0xffffffffu, mbar_wait_hot(bar, par, abort_flag, a.err,
-                                                   kErrPrefillWait)) != 0;
-    };
-    each_share([&](const Share& me) {
-      for (int nt = me.nt_beg; nt < me.nt_end; ++nt, ++U) {
-        const bool held = nt * BN + key >= me.key_beg && nt * BN + key < me.key_end;
-        const uint32_t buf = U & 1u;
+    passes([&](auto half_type) {
+      constexpr bool H = decltype(half_type)::value, W = H && !F16;
+      // A thread takes one key and half of the dims: NG / 2 groups.  Eight
+      // consecutive keys in a quarter-warp: neither the records' 16 (D / 32 +
+      // 1)-byte rows nor the swizzled 16-byte stores conflict.
+      constexpr int G2 = NG / 2;
+      const int key = static_cast<int>(threadIdx.x) & 127;
+      const int half = static_cast<int>(threadIdx.x - 256) >> 7;
+      const uint32_t swz = static_cast<uint32_t>(key & 7) << 4;
+      const uint32_t raw_at = smem_u32(raw) + key * P;
+      const uint32_t row_at =
+          smem_u32(smem) + (CH == 2 ? half * L::kChunkBytes : half * 64) + key * 128;
+      const uint32_t k_at = row_at + L::k_off(nq), v_at = row_at + L::v_off(nq);
+      uint32_t U = 0;  // key tiles unpacked
+      int s = 0;
+      uint32_t parity = 0;
+      uint32_t most = 0u, least = ~0u;  // W: the records' parameters so far (see kMostScale)
+      auto wait = [&](uint64_t* bar, uint32_t par) {
+        return __all_sync(0xffffffffu, mbar_wait_hot(bar, par, abort_flag, a.err,
+                                                     kErrPrefillWait)) != 0;
+      };
+      each_share([&](const Share& me) {
+        for (int nt = me.nt_beg; nt < me.nt_end; ++nt, ++U) {
+          const bool held = nt * BN + key >= me.key_beg && nt * BN + key < me.key_end;
+          const uint32_t buf = U & 1u;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {  // K, then V
-          if (!wait(&raw_full[s], parity)) return false;
-          uint32_t par[G2];
-          uint4 code[G2];
+          for (int x = 0; x < 2; ++x) {  // K, then V
+            if (!wait(&raw_full[s], parity)) return false;
+            uint32_t par[G2];
+            uint4 code[G2];
 #pragma unroll
-          for (int i = 0; i < G2; ++i) {
-            par[i] = ld_shared(raw_at + s * L::kRaw + (half * G2 + i) * 4);
-            code[i] = ld_shared4(raw_at + s * L::kRaw + kHeadBytes + (half * G2 + i) * 16);
-          }
-          // The stage goes back to the producer, whose next copy overwrites it.
-          // Three things stand between the loads above and that copy: the loads
-          // are generic accesses and the copy is one of the async proxy, which
-          // the mbarrier alone does not order (the proxy fence); they are 32
-          // lanes' and the arrival is lane 0's (__syncwarp, which a vote does not
-          // replace); and the words are in registers (the branch, never taken).
-          // Without the fence and the branch, results at head dim 128 changed
-          // from call to call.
-          uint32_t any = 0u;
-#pragma unroll
-          for (int i = 0; i < G2; ++i)
-            any ^= par[i] ^ code[i].x ^ code[i].y ^ code[i].z ^ code[i].w;
-          if (__any_sync(0xffffffffu, any == 0xA5A5A5A5u)) __nanosleep(0);
-          fence_proxy_async_smem();
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < G2; ++i)
-            if (!held) par[i] = 0u;  // seen by no row: zeros, whatever is there
-          if (lane == 0) mbar_arrive(&raw_empty[s]);
-          if (++s == R) {
-            s = 0;
-            parity ^= 1u;
-          }
-          uint64_t* const empty = x == 0 ? &k_empty[buf] : &v_empty[buf];
-          if (U >= 2 && !wait(empty, ((U >> 1) - 1) & 1u)) return false;
-          const uint32_t to = (x == 0 ? k_at : v_at) + buf * L::kTile;
-#pragma unroll
-          for (int i = 0; i < G2; ++i) {
-            const uint32_t scale2 = __byte_perm(par[i], 0u, 0x1010);
-            const uint32_t min2 = __byte_perm(par[i], 0u, 0x3232);
-            const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t v[4];
-              values_of<F16>(v, w[j], scale2, min2);
-              uint4 out;
-              if (x == 0) {  // dims in order
-                out.x = __byte_perm(v[0], v[1], 0x5410);
-                out.y = __byte_perm(v[2], v[3], 0x5410);
-                out.z = __byte_perm(v[0], v[1], 0x7632);
-                out.w = __byte_perm(v[2], v[3], 0x7632);
-              } else {       // as the nibbles fall
-                out = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-              // (half * 64 is a multiple of 64 and swz of 16: the XOR of the
-              // piece's number stays inside the row's 128 bytes.)
-              st_shared4((to + (i * 4 + j) * 16) ^ swz, out);
+            for (int i = 0; i < G2; ++i) {
+              par[i] = ld_shared(raw_at + s * L::kRaw + (half * G2 + i) * 4);
+              code[i] = ld_shared4(raw_at + s * L::kRaw + kHeadBytes + (half * G2 + i) * 16);
             }
+            // The stage goes back to the producer, whose next copy overwrites it.
+            // Three things stand between the loads above and that copy: the loads
+            // are generic accesses and the copy is one of the async proxy, which
+            // the mbarrier alone does not order (the proxy fence); they are 32
+            // lanes' and the arrival is lane 0's (__syncwarp, which a vote does not
+            // replace); and the words are in registers (the branch, never taken).
+            // Without the fence and the branch, results at head dim 128 changed
+            // from call to call.
+            uint32_t any = 0u;
+#pragma unroll
+            for (int i = 0; i < G2; ++i)
+              any ^= par[i] ^ code[i].x ^ code[i].y ^ code[i].z ^ code[i].w;
+            if (__any_sync(0xffffffffu, any == 0xA5A5A5A5u)) __nanosleep(0);
+            fence_proxy_async_smem();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < G2; ++i)
+              if (!held) par[i] = 0u;  // seen by no row: zeros, whatever is there
+            if (lane == 0) mbar_arrive(&raw_empty[s]);
+            if (++s == R) {
+              s = 0;
+              parity ^= 1u;
+            }
+            if (W) {
+#pragma unroll
+              for (int i = 0; i < G2; ++i) {
+                most = max_bf16x2(most, par[i] & 0x7FFF7FFFu);
+                const uint32_t up = mul_bf16x2(par[i], kUp2);
+                const float scale = __uint_as_float(up << 16);
+                const float low = __uint_as_float(up & 0xFFFF0000u);
+                // (The bits less one, so that a group of zeros counts as large.)
+                if (x == 1)
+                  least = min(least, __float_as_uint(fmaxf(8.f * scale, fabsf(low))) - 1u);
+                par[i] = pack_f16x2(scale, low);
+              }
+            }
+            uint64_t* const empty = x == 0 ? &k_empty[buf] : &v_empty[buf];
+            if (U >= 2 && !wait(empty, ((U >> 1) - 1) & 1u)) return false;
+            const uint32_t to = (x == 0 ? k_at : v_at) + buf * L::kTile;
+#pragma unroll
+            for (int i = 0; i < G2; ++i) {
+              const uint32_t scale2 = __byte_perm(par[i], 0u, 0x1010);
+              const uint32_t min2 = __byte_perm(par[i], 0u, 0x3232);
+              const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t v[4];
+                values_of<H>(v, w[j], scale2, min2);
+                uint4 out;
+                if (x == 0) {  // dims in order
+                  out.x = __byte_perm(v[0], v[1], 0x5410);
+                  out.y = __byte_perm(v[2], v[3], 0x5410);
+                  out.z = __byte_perm(v[0], v[1], 0x7632);
+                  out.w = __byte_perm(v[2], v[3], 0x7632);
+                } else {       // as the nibbles fall
+                  out = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                // (half * 64 is a multiple of 64 and swz of 16: the XOR of the
+                // piece's number stays inside the row's 128 bytes.)
+                st_shared4((to + (i * 4 + j) * 16) ^ swz, out);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x == 0 ? &k_full[buf] : &v_full[buf]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(x == 0 ? &k_full[buf] : &v_full[buf]);
         }
-      }
-      return true;
+        return true;
+      });
+      if (W && ((most & 0xFFFFu) >= kMostScale || (most >> 16) >= kMostMin || least < kLeast))
+        *redo = 1;
     });
   } else {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int X = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + X * BN;
-    const uint32_t o_col = tmem + lane_base + kOCol;  // O_0's
-    const int hh = row / ca.qpt, qi = row % ca.qpt;
-    const bool live = (warp & 3) * 32 < ca.rows;  // a warp without rows only keeps step
-    uint32_t J = 0, n_share = 0, n_trade = 0;
-    bool first_share = true;
-    each_share([&](const Share& me) {
-      Pair pr = me.pr;
-      if (nq == 2) pr.mt0 += X;
-      const Slot sl = slot_of(pr, a, ca.qpt);
-      const int q = sl.q0 + qi;
-      const bool row_valid = row < ca.rows && q < a.Sq;
-      // Keys [row_lo, row_hi) that this row sees, and key tiles [all_beg,
-      // all_end) that every row sees all of.
-      int row_lo = 0, row_hi = pr.len, all_beg = 0, all_end = pr.len / BN;
-      if (a.causal) {
-        const int64_t off = pair_off(a, pr);
-        row_hi = static_cast<int>(imax64(0, imin64(row_hi, q + off + 1)));
-        all_end = static_cast<int>(imax64(0, imin64(pr.len, sl.q0 + off + 1)) / BN);
-        if (a.window > 0) {
-          row_lo = static_cast<int>(imin64(row_hi, imax64(0, q + off - a.window + 1)));
-          all_beg = static_cast<int>(
-              imin64(all_end, (imax64(0, sl.q_last + off - a.window + 1) + BN - 1) / BN));
+    passes([&](auto half) {
+      constexpr bool H = decltype(half)::value, W = H && !F16;
+      const int X = warp >> 2;
+      const int row = (warp & 3) * 32 + lane;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_col = tmem + lane_base + X * BN;
+      const uint32_t o_col = tmem + lane_base + kOCol;  // O_0's
+      const int hh = row / ca.qpt, qi = row % ca.qpt;
+      const bool live = (warp & 3) * 32 < ca.rows;  // a warp without rows only keeps step
+      uint32_t J = 0, n_share = 0, n_trade = 0;
+      bool first_share = true;
+      each_share([&](const Share& me) {
+        Pair pr = me.pr;
+        if (nq == 2) pr.mt0 += X;
+        const Slot sl = slot_of(pr, a, ca.qpt);
+        const int q = sl.q0 + qi;
+        const bool row_valid = row < ca.rows && q < a.Sq;
+        // Keys [row_lo, row_hi) that this row sees, and key tiles [all_beg,
+        // all_end) that every row sees all of.
+        int row_lo = 0, row_hi = pr.len, all_beg = 0, all_end = pr.len / BN;
+        if (a.causal) {
+          const int64_t off = pair_off(a, pr);
+          row_hi = static_cast<int>(imax64(0, imin64(row_hi, q + off + 1)));
+          all_end = static_cast<int>(imax64(0, imin64(pr.len, sl.q0 + off + 1)) / BN);
+          if (a.window > 0) {
+            row_lo = static_cast<int>(imin64(row_hi, imax64(0, q + off - a.window + 1)));
+            all_beg = static_cast<int>(
+                imin64(all_end, (imax64(0, sl.q_last + off - a.window + 1) + BN - 1) / BN));
+          }
         }
-      }
-      float m_ref = -INFINITY, l = 0.f;
-      bool ok = true;
-      bool begun = false;  // O_X holds something of this share
-      for (int nt = me.nt_beg + (nq == 1 ? X : 0); nt < me.nt_end; nt += 3 - nq) {
-        // (Warp-uniform: every TMEM access below is made by the whole warp.)
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait_hot(&s_full[X], J & 1u, abort_flag, a.err, kErrPrefillWait));
-        ++J;
-        if (!ok) break;
-        if (live) {
-          // Wholly visible tiles work on raw scores and fold the scale into one
-          // FMA per element; the others test each key.
-          const bool fast = nt >= all_beg && nt < all_end && a.scale_log2 >= 0.f;
-          uint32_t r[BN];
-          tc_fence_after();
+        bool ok = true;
+        // Base-2 scores per score of the products (W: without Q's and K's powers).
+        float to_log2 = a.scale_log2;
+        if (W && me.nt_end > me.nt_beg) {
+          // The row of Q in fp16, times the power of two that brings its largest
+          // element to [2^14, 2^15): exact down to 2^-28 of that.  With one query
+          // tile a row's two threads, who both need the power, take half each.
+          if (live) {
+            ok = __all_sync(0xffffffffu, mbar_wait_hot(q_full, n_share & 1u, abort_flag, a.err,
+                                                       kErrPrefillWait));
+            const uint32_t q_at = smem_u32(smem) + (nq == 2 ? X * L::kTile : 0) + row * 128;
+            const uint32_t swz = static_cast<uint32_t>(row & 7) << 4;
+            auto piece = [&](int i) {
+              return q_at + (i >> 3) * L::kChunkBytes + (((i & 7) << 4) ^ swz);
+            };
+            uint32_t big = 0u;
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
-            tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[c * 32]));
-          tmem_ld_wait();
-          if (!fast) {
-            const int lo = row_lo - nt * BN, hi = row_hi - nt * BN;
-#pragma unroll
-            for (int c = 0; c < BN; ++c)
-              r[c] = __float_as_uint(c >= lo && c < hi ? __uint_as_float(r[c]) * a.scale_log2
-                                                       : -INFINITY);
-          }
-          float part[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) part[e] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < BN; c += 16)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              part[e] = fmax3(part[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + 8 + e]));
-          float mx = fmax3(fmax3(part[0], part[1], part[2]), fmax3(part[3], part[4], part[5]),
-                           fmaxf(part[6], part[7]));
-          if (fast) mx *= a.scale_log2;
-          const float m_new = fmaxf(m_ref, mx);
-          const bool grow = m_new > m_ref + kRescaleLog2;  // also for -inf -> finite
-          const float alpha = grow ? fast_exp2(m_ref - m_new) : 1.f;
-          const bool o_live = grow && begun && m_ref != -INFINITY;
-          if (grow) {
-            l *= alpha;
-            m_ref = m_new;
-          }
-          const float ref = exp_ref(m_ref);
-          const float sc = fast ? a.scale_log2 : 1.f;
-          const float up = kWeightLog2 - ref;
-          const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(up, up);
-          uint64_t lp[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) lp[e] = 0;
-#pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int c0 = c * 32 + 2 * e;
-              const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[c0]), __uint_as_float(r[c0 + 1])),
-                                        sc2, nref2);
-              const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
-              lp[e & 3] = f2_add(lp[e & 3], f2_pack(p0, p1));
-              pk[e] = pack2<F16>(p0, p1);
+            for (int i = 0; i < 8 * CH; ++i) {
+              const uint4 v = ld_shared4(piece(i));
+              big = __vmaxu2(big, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                           __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
             }
-            tmem_st16(s_col + c * 16, pk);
-          }
-          l += ((f2_lo(lp[0]) + f2_hi(lp[0])) + (f2_lo(lp[1]) + f2_hi(lp[1]))) +
-               ((f2_lo(lp[2]) + f2_hi(lp[2])) + (f2_lo(lp[3]) + f2_hi(lp[3])));
-          if (__any_sync(0xffffffffu, o_live)) {
-            // O_X holds the earlier tiles' P V with the old reference; they are
-            // done (S_X follows them) and the next PV_X waits for this P.
-            const float f = o_live ? alpha : 1.f;
+            if (nq == 1) ok = bar_and(1 + (warp & 3), 64, ok);  // both have read the row
+            const int top = static_cast<int>(max(big & 0xFFFFu, big >> 16) >> 7);
+            const int e = top == 0 || top == 255 ? 0 : min(14 + 127 - top, 126);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            to_log2 *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * (1.f / kUp);
+            if (top != 0 && !(fabsf(to_log2) <= kMostToLog2)) *redo = 1;
+            const int i0 = nq == 1 ? X * 4 * CH : 0, i1 = nq == 1 ? i0 + 4 * CH : 8 * CH;
+            for (int i = i0; i < i1; ++i) {
+              uint4 v = ld_shared4(piece(i));
+              uint32_t* w = &v.x;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(o_col + X * 128 + c * 32, o);
+              for (int x = 0; x < 4; ++x)
+                w[x] = pack_f16x2(__uint_as_float(w[x] << 16) * up,
+                                  __uint_as_float(w[x] & 0xFFFF0000u) * up);
+              st_shared4(piece(i), v);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(q_ready);
+          if (!ok) return false;
+        }
+        float m_ref = -INFINITY, l = 0.f;
+        bool begun = false;  // O_X holds something of this share
+        for (int nt = me.nt_beg + (nq == 1 ? X : 0); nt < me.nt_end; nt += 3 - nq) {
+          // (Warp-uniform: every TMEM access below is made by the whole warp.)
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait_hot(&s_full[X], J & 1u, abort_flag, a.err, kErrPrefillWait));
+          ++J;
+          if (!ok) break;
+          if (live) {
+            // Wholly visible tiles work on raw scores and fold the scale into one
+            // FMA per element; the others test each key.
+            const bool fast = nt >= all_beg && nt < all_end && a.scale_log2 >= 0.f;
+            uint32_t r[BN];
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c)
+              tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[c * 32]));
+            tmem_ld_wait();
+            if (!fast) {
+              const int lo = row_lo - nt * BN, hi = row_hi - nt * BN;
+#pragma unroll
+              for (int c = 0; c < BN; ++c)
+                r[c] = __float_as_uint(c >= lo && c < hi ? __uint_as_float(r[c]) * to_log2
+                                                         : -INFINITY);
+            }
+            float part[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part[e] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < BN; c += 16)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                part[e] = fmax3(part[e], __uint_as_float(r[c + e]), __uint_as_float(r[c + 8 + e]));
+            float mx = fmax3(fmax3(part[0], part[1], part[2]), fmax3(part[3], part[4], part[5]),
+                             fmaxf(part[6], part[7]));
+            if (fast) mx *= to_log2;
+            const float m_new = fmaxf(m_ref, mx);
+            const bool grow = m_new > m_ref + kRescaleLog2;  // also for -inf -> finite
+            const float alpha = grow ? fast_exp2(m_ref - m_new) : 1.f;
+            const bool o_live = grow && begun && m_ref != -INFINITY;
+            if (grow) {
+              l *= alpha;
+              m_ref = m_new;
+            }
+            const float ref = exp_ref(m_ref);
+            const float sc = fast ? to_log2 : 1.f;
+            const float up = kWeightLog2 - ref;
+            const uint64_t sc2 = f2_pack(sc, sc), nref2 = f2_pack(up, up);
+            uint64_t lp[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) lp[e] = 0;
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int c0 = c * 32 + 2 * e;
+                const uint64_t x = f2_fma(
+                    f2_pack(__uint_as_float(r[c0]), __uint_as_float(r[c0 + 1])), sc2, nref2);
+                const float p0 = fast_exp2(f2_lo(x)), p1 = fast_exp2(f2_hi(x));
+                lp[e & 3] = f2_add(lp[e & 3], f2_pack(p0, p1));
+                pk[e] = pack2<H>(p0, p1);
+              }
+              tmem_st16(s_col + c * 16, pk);
+            }
+            l += ((f2_lo(lp[0]) + f2_hi(lp[0])) + (f2_lo(lp[1]) + f2_hi(lp[1]))) +
+                 ((f2_lo(lp[2]) + f2_hi(lp[2])) + (f2_lo(lp[3]) + f2_hi(lp[3])));
+            if (__any_sync(0xffffffffu, o_live)) {
+              // O_X holds the earlier tiles' P V with the old reference; they are
+              // done (S_X follows them) and the next PV_X waits for this P.
+              const float f = o_live ? alpha : 1.f;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_col + X * 128 + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_col + X * 128 + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+                tmem_st16(o_col + X * 128 + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+              }
+            }
+            begun = true;
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[X]);
+        }
+        // Epilogue: out, or this CTA's partial of a split group.
+        const bool some = me.nt_end > me.nt_beg;
+        const bool split = me.c_lo != me.c_hi;
+        ok = __all_sync(0xffffffffu, ok && (!some || mbar_wait_hot(o_final, n_share & 1u, abort_flag,
+                                                                   a.err, kErrPrefillWait)));
+        // Weights of O_0 and O_1 in this row's result.
+        float w0 = X == 0 ? 1.f : 0.f, w1 = X == 0 ? 0.f : 1.f;
+        if (nq == 1 && live) {
+          // The row's two threads trade their states and take half of the columns
+          // each.  (A warp that has failed meets its partner here once more.)
+          float2* at = xch + (n_trade & 1u) * 256;
+          ++n_trade;
+          at[X * 128 + row] = make_float2(m_ref, l);
+          ok = bar_and(1 + (warp & 3), 64, ok);
+          const float2 other = at[(X ^ 1) * 128 + row];
+          const float M = fmaxf(m_ref, other.x), ref = exp_ref(M);
+          const float wm = fast_exp2(m_ref - ref), wo = fast_exp2(other.x - ref);
+          l = wm * l + wo * other.y;
+          m_ref = M;
+          w0 = X == 0 ? wm : wo;
+          w1 = X == 0 ? wo : wm;
+        }
+        if (!ok) return false;
+        const int slot = cta * 2 + (first_share ? 0 : 1);
+        first_share = false;
+        if (threadIdx.x == 0 && (!split || me.opens))
+          ca.info[me.id] = split ? make_int2(slot, me.c_hi - me.c_lo + 1) : make_int2(0, 1);
+        // O_X exists if X had a tile in this share.
+        const bool has0 = some && (nq == 1 || X == 0);
+        const bool has1 = nq == 1 ? me.nt_end - me.nt_beg > 1 : some && X == 1;
+        const int64_t pat = (static_cast<int64_t>(slot) * nq + (nq == 2 ? X : 0)) * BM + row;
+        if (split && row_valid && (nq == 2 || X == 0)) ca.part_ml[pat] = make_float2(m_ref, l);
+        const float inv = split ? 1.f : 1.f / l;  // no visible key: 0 * inf = NaN
+        w0 *= W ? inv * (1.f / kUp) : inv;
+        w1 *= W ? inv * (1.f / kUp) : inv;
+        constexpr int kCols = D / 32;  // 32-column pieces
+        const int c_beg = nq == 1 ? X * (kCols / 2) : 0;
+        const int c_end = nq == 1 ? c_beg + kCols / 2 : kCols;
+        for (int c = c_beg; c < c_end; ++c) {
+          __syncwarp();  // (the TMEM loads below are the whole warp's)
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f * inv;
+          if (live) {
+            uint32_t r[32];
+            tc_fence_after();
+            if (has0) {
+              tmem_ld32(o_col + c * 32, r);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st16(o_col + X * 128 + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-              tmem_st16(o_col + X * 128 + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
+            }
+            if (has1) {
+              tmem_ld32(o_col + 128 + c * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = has0 ? fmaf(__uint_as_float(r[e]), w1, o[e]) : __uint_as_float(r[e]) * w1;
+            }
+            tc_fence_before();
+          }
+          if (!row_valid) continue;
+          // O's columns are the dims with each eight as V's nibbles fell.
+          constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // column of dim e of eight
+          if (split) {
+            float* po = ca.part_o + pat * D + c * 32;
+#pragma unroll
+            for (int d = 0; d < 32; d += 8)
+#pragma unroll
+              for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4*>(po + d + e) =
+                    make_float4(o[d + kAt[e]], o[d + kAt[e + 1]], o[d + kAt[e + 2]],
+                                o[d + kAt[e + 3]]);
+          } else {
+            uint16_t* orow = a.out + pr.b * a.os[0] + static_cast<int64_t>(pr.kv * a.g + hh) * a.os[1] +
+                             static_cast<int64_t>(q) * a.os[2] + c * 32;
+#pragma unroll
+            for (int d = 0; d < 32; d += 8) {
+              if (c * 32 + d >= a.Dv) break;
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack2<F16>(o[d + kAt[2 * e]], o[d + kAt[2 * e + 1]]);
+              *reinterpret_cast<uint4*>(orow + d) = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          begun = true;
-          tmem_st_wait();
-          tc_fence_before();
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[X]);
-      }
-      // Epilogue: out, or this CTA's partial of a split group.
-      const bool some = me.nt_end > me.nt_beg;
-      const bool split = me.c_lo != me.c_hi;
-      ok = __all_sync(0xffffffffu, ok && (!some || mbar_wait_hot(o_final, n_share & 1u, abort_flag,
-                                                                 a.err, kErrPrefillWait)));
-      // Weights of O_0 and O_1 in this row's result.
-      float w0 = X == 0 ? 1.f : 0.f, w1 = X == 0 ? 0.f : 1.f;
-      if (nq == 1 && live) {
-        // The row's two threads trade their states and take half of the columns
-        // each.  (A warp that has failed meets its partner here once more.)
-        float2* at = xch + (n_trade & 1u) * 256;
-        ++n_trade;
-        at[X * 128 + row] = make_float2(m_ref, l);
-        ok = bar_and(1 + (warp & 3), 64, ok);
-        const float2 other = at[(X ^ 1) * 128 + row];
-        const float M = fmaxf(m_ref, other.x), ref = exp_ref(M);
-        const float wm = fast_exp2(m_ref - ref), wo = fast_exp2(other.x - ref);
-        l = wm * l + wo * other.y;
-        m_ref = M;
-        w0 = X == 0 ? wm : wo;
-        w1 = X == 0 ? wo : wm;
-      }
-      if (!ok) return false;
-      const int slot = cta * 2 + (first_share ? 0 : 1);
-      first_share = false;
-      if (threadIdx.x == 0 && (!split || me.opens))
-        ca.info[me.id] = split ? make_int2(slot, me.c_hi - me.c_lo + 1) : make_int2(0, 1);
-      // O_X exists if X had a tile in this share.
-      const bool has0 = some && (nq == 1 || X == 0);
-      const bool has1 = nq == 1 ? me.nt_end - me.nt_beg > 1 : some && X == 1;
-      const int64_t pat = (static_cast<int64_t>(slot) * nq + (nq == 2 ? X : 0)) * BM + row;
-      if (split && row_valid && (nq == 2 || X == 0)) ca.part_ml[pat] = make_float2(m_ref, l);
-      const float inv = split ? 1.f : 1.f / l;  // no visible key: 0 * inf = NaN
-      w0 *= inv;
-      w1 *= inv;
-      constexpr int kCols = D / 32;  // 32-column pieces
-      const int c_beg = nq == 1 ? X * (kCols / 2) : 0;
-      const int c_end = nq == 1 ? c_beg + kCols / 2 : kCols;
-      for (int c = c_beg; c < c_end; ++c) {
-        __syncwarp();  // (the TMEM loads below are the whole warp's)
-        float o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f * inv;
-        if (live) {
-          uint32_t r[32];
-          tc_fence_after();
-          if (has0) {
-            tmem_ld32(o_col + c * 32, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(r[e]) * w0;
-          }
-          if (has1) {
-            tmem_ld32(o_col + 128 + c * 32, r);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = has0 ? fmaf(__uint_as_float(r[e]), w1, o[e]) : __uint_as_float(r[e]) * w1;
-          }
-          tc_fence_before();
+        if (some) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+          ++n_share;
         }
-        if (!row_valid) continue;
-        // O's columns are the dims with each eight as V's nibbles fell.
-        constexpr int kAt[8] = {0, 2, 4, 6, 1, 3, 5, 7};  // column of dim e of eight
-        if (split) {
-          float* po = ca.part_o + pat * D + c * 32;
-#pragma unroll
-          for (int d = 0; d < 32; d += 8)
-#pragma unroll
-            for (int e = 0; e < 8; e += 4)
-              *reinterpret_cast<float4*>(po + d + e) =
-                  make_float4(o[d + kAt[e]], o[d + kAt[e + 1]], o[d + kAt[e + 2]],
-                              o[d + kAt[e + 3]]);
-        } else {
-          uint16_t* orow = a.out + pr.b * a.os[0] + static_cast<int64_t>(pr.kv * a.g + hh) * a.os[1] +
-                           static_cast<int64_t>(q) * a.os[2] + c * 32;
-#pragma unroll
-          for (int d = 0; d < 32; d += 8) {
-            if (c * 32 + d >= a.Dv) break;
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack2<F16>(o[d + kAt[2 * e]], o[d + kAt[2 * e + 1]]);
-            *reinterpret_cast<uint4*>(orow + d) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      if (some) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-        ++n_share;
-      }
-      return true;
+        return true;
+      });
     });
   }
   tc_fence_before();

@@ -377,10 +377,11 @@ GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const v
  * paged caches, empty problems, rows without a visible key, the workspace and
  * the errors are those of gqa_forward.
  * Short query blocks (GQA_KERNEL_Q4) multiply the 4-bit codes themselves and
- * round neither keys nor values; longer ones round each key and value once to
- * the 16-bit type, on the way to the tensor cores (GQA_KERNEL_Q4_CHUNK) or in
- * scratch (GQA_KERNEL_Q4_PREFILL; part of plan.workspace_bytes, at most 1 GiB
- * unless one head's keys alone need more).  What decides is the estimated time
+ * round neither keys nor values; longer ones round each key, value and weight
+ * once to 16 bits, on the way to the tensor cores (GQA_KERNEL_Q4_CHUNK: to fp16,
+ * or to bf16 where a bf16 cache's values or queries are past what fp16 holds) or
+ * in scratch (GQA_KERNEL_Q4_PREFILL: to the cache's type; part of
+ * plan.workspace_bytes, at most 1 GiB unless one head's keys alone need more).  What decides is the estimated time
  * of each; a single token always takes the first.
  * A key that no query of the block can see by lengths, diagonal and window
  * never reaches the result, whatever its record holds.  One that some query

@@ -299,7 +299,86 @@ def test_scales_and_blocks_without_a_diagonal(gqa, Sq, masked, causal, dtype, ke
             assert torch.all(err <= bound), float((err / bound).max())
 
 
-@pytest.mark.parametrize("dtype", ["fp16"])
+def _chunk_case(gqa, D, Sq, Sk, kf, vf, qf, seed, dtype="bf16", groups=None):
+    """A block whose K, V and Q are kf, vf and qf times normal numbers (groups:
+    factors of V's groups of 32 dims); attention in 64 bits over the records,
+    and each element's bound with keys, values and weights rounded to `unit`."""
+    B, Hq, Hkv = 2, 8, 2
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    caches, values = [], []
+    for f, parts in ((kf, None), (vf, groups)):
+        x = torch.randn(B, Hkv, Sk, D, generator=gen, device="cuda") * f
+        if parts:
+            for i, y in enumerate(parts):
+                x[..., 32 * i:32 * i + 32] *= y
+        x = x.to(u.TORCH[dtype])
+        c = torch.zeros(B, Hkv, Sk, u.record_bytes(D), dtype=torch.uint8, device="cuda")
+        gqa.kv_append_q4(c, c.clone(), x, x, torch.zeros(B, dtype=torch.int32, device="cuda"))
+        G = -(-D // 32)
+        par = c[..., :4 * G].contiguous().view(u.TORCH[dtype]).double().unflatten(-1, (G, 2))
+        code = torch.stack([c[..., 16:] % 16, c[..., 16:] // 16], -1).double().flatten(-2)
+        caches.append(c)
+        values.append((code.unflatten(-1, (G, 32)) * par[..., :1] + par[..., 1:]).flatten(-2)[..., :D])
+    q = (torch.randn(B, Hq, Sq, D, generator=gen, device="cuda") * qf).to(u.TORCH[dtype])
+    kw = dict(causal=True, causal_offset="bottom_right", scale=1.0 / (kf * qf * math.sqrt(D)))
+    assert gqa.query_q4(q, *caches, **kw)["kernel_name"] == "q4_chunk"
+    see = torch.arange(Sk, device="cuda") <= torch.arange(Sq, device="cuda")[:, None] + Sk - Sq
+    ref, move, size = [], [], []
+    for b in range(B):
+        for h in range(Hq):
+            k, v, qh = values[0][b, h // 4], values[1][b, h // 4], q[b, h].double()
+            p = torch.softmax((qh @ k.T * kw["scale"]).masked_fill(~see, -math.inf), -1)
+            ref.append(p @ v)
+            size.append(p @ v.abs())
+            move.append(kw["scale"] * (qh.abs() @ k.abs().T).amax(-1, keepdim=True))
+    ref, size = (torch.stack(x).view(B, Hq, Sq, D) for x in (ref, size))
+    move = torch.stack(move).view(B, Hq, Sq, 1)
+
+    def bound(unit, out):
+        return size * (2.02 * unit + 2.1 * unit * move + 2.0 ** -14) + 1.01 * out * ref.abs()
+
+    return q, caches, kw, ref, bound
+
+
+@pytest.mark.parametrize("D,Sq,Sk", [(128, 512, 2048), (128, 20, 20000), (64, 300, 4000),
+                                     (96, 777, 3333)])
+def test_bf16_chunks_keep_more_bits_than_bf16(gqa, D, Sq, Sk):
+    """bf16 caches are multiplied in fp16 operands: what is off is the result's
+    own rounding, in norm within a quarter."""
+    q, caches, kw, ref, bound = _chunk_case(gqa, D, Sq, Sk, 1.0, 1.0, 1.0, 41)
+    out = gqa.forward_q4(q, *caches, **kw)
+    assert gqa.device_status() == gqa.GQA_OK
+    err = (out.double() - ref).abs()
+    # fp16 roundings of keys, values and weights, bf16's of the result.
+    assert torch.all(err <= bound(2.0 ** -11, 2.0 ** -8))
+    own = (ref.bfloat16().double() - ref).norm()
+    assert float(err.norm() / own) <= 1.25
+
+
+@pytest.mark.parametrize("D,Sq,Sk", [(128, 512, 2048), (64, 32, 16384)])
+@pytest.mark.parametrize("kf,vf,qf,groups", [
+    (1.0, 1e-6, 1.0, None), (1.0, 3e4, 1.0, None), (1.0, 1e30, 1.0, None),
+    (1e-7, 1.0, 1e7, None), (1e9, 1.0, 1e-9, None), (300.0, 40.0, 1e-20, None),
+    (1.0, 1.0, 1e20, None), (1.0, 1.0, 1.0, [1.0, 2.0 ** -18]), (1.0, 1.0, 1.0, [2.0 ** 12, 1.0]),
+])
+def test_bf16_chunks_of_any_size(gqa, kf, vf, qf, groups, D, Sq, Sk):
+    """Keys, values or queries that fp16 would not hold come out as bf16
+    operands give them, and the next call is as before."""
+    q, caches, kw, ref, bound = _chunk_case(gqa, D, Sq, Sk, kf, vf, qf, 42, groups=groups)
+    plan = gqa.query_q4(q, *caches, **kw)
+    nq, nc, nkw, nref, nbound = _chunk_case(gqa, D, Sq, Sk, 1.0, 1.0, 1.0, 43)
+    ws = torch.zeros(plan["workspace_bytes"], dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        out = gqa.forward_q4(q, *caches, workspace=ws, **kw).double()
+        err = (out - ref).abs()
+        assert torch.all(err <= bound(2.0 ** -8, 2.0 ** -8)), float((err / bound(2.0 ** -8, 2.0 ** -8)).max())
+        assert not ws[:256].any()
+        out = gqa.forward_q4(nq, *nc, workspace=ws, **nkw).double()
+        assert torch.all((out - nref).abs() <= nbound(2.0 ** -11, 2.0 ** -8))
+    assert gqa.device_status(ws) == gqa.GQA_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("share", [2.0 ** -6, 2.0 ** -14])
 def test_weight_on_a_key_of_zeros(gqa, dtype, share):
     """Nearly all weight on one key whose values are zeros, as heads that have
