@@ -40,6 +40,7 @@ GQA_ERR_NULL, GQA_ERR_SHAPE, GQA_ERR_LAYOUT, GQA_ERR_UNSUPPORTED = 1, 2, 3, 4
 GQA_ERR_WORKSPACE, GQA_ERR_CUDA, GQA_ERR_TIMEOUT, GQA_ERR_ARG, GQA_ERR_DEVICE = 5, 6, 7, 8, 9
 GQA_ERR_SCRATCH_LIMIT, GQA_ERR_KV_LENGTH, GQA_ERR_PAGE = 10, 11, 12
 STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
+WORKSPACE_HEAD_BYTES = 65792
 GQA_DTYPE_BF16, GQA_DTYPE_F32, GQA_DTYPE_F16 = 0, 1, 2
 KERNEL_NAMES = {0: "none", 1: "decode", 2: "prefill", 3: "f32", 4: "zero", 5: "nan", 6: "q4",
                 7: "q4_prefill", 8: "q4_chunk"}

@@ -34,6 +34,7 @@ constexpr int64_t kMaxRaggedBatch = 16384;  // batch entries with per-sequence l
 constexpr int64_t kWorkspaceHeadBytes = 256;
 constexpr int64_t kCounterRegionBytes = 64 * 1024;
 constexpr int64_t kScratchOffset = kWorkspaceHeadBytes + kCounterRegionBytes;
+static_assert(kScratchOffset == GQA_WORKSPACE_HEAD_BYTES, "what the header says has to be zero");
 
 // Keys [lo, hi) of one batch entry that some query of the block can see,
 // and the decode key tiles [t0, t0 + tiles) that hold them.  `len` is the entry's

@@ -17,8 +17,9 @@ import ctypes
 import math
 import threading
 
-from . import (GQA_DTYPE_BF16, GQA_DTYPE_F16, GQA_OK, GQAError, Plan, Problem, _lens_ptr, _lib,
-               _offset, _stream_object, _table, _torch, _workspaces, make_problem, workspace_for)
+from . import (GQA_DTYPE_BF16, GQA_DTYPE_F16, GQA_OK, WORKSPACE_HEAD_BYTES, GQAError, Plan,
+               Problem, _lens_ptr, _lib, _offset, _stream_object, _table, _torch, _workspaces,
+               make_problem, workspace_for)
 
 _vp = ctypes.c_void_p
 
@@ -144,9 +145,6 @@ def _elsewhere(idx, stream):
     return stack
 
 
-_HEAD = 256 + 65536  # error word, append ticket and decode tickets: what has to start at zero
-
-
 def _workspace(idx, stream, nbytes, workspace):
     """The caller's workspace, the cached one of the current stream, or, in a
     capture, one that belongs to the graph alone (zeroed by each replay):
@@ -156,7 +154,7 @@ def _workspace(idx, stream, nbytes, workspace):
     if _capturing():
         torch = _torch()
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", idx))
-        ws[:_HEAD].zero_()
+        ws[:WORKSPACE_HEAD_BYTES].zero_()
         return ws
     ws = _workspaces.get((idx, stream))
     if ws is None or ws.numel() < nbytes:

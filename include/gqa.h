@@ -174,8 +174,8 @@ GQA_API int gqa_query(const gqa_problem* p, int sm_count, gqa_plan* plan);
  *   mask:         device uint8 pointer if p->has_mask, else ignored (may be NULL).
  *   workspace:    device scratch of at least plan.workspace_bytes, 256-byte
  *                 aligned, owned by the caller, ZERO-FILLED before its first
- *                 use.  Its head holds the error word and the decode ticket
- *                 counters (bytes [256, 256 + 64 KiB)); every call leaves that
+ *                 use.  Its head (GQA_WORKSPACE_HEAD_BYTES) holds the error word
+ *                 and, from byte 256 on, the decode ticket counters; every call leaves that
  *                 head as it found it, so one workspace serves any sequence
  *                 of calls of any shapes without being cleared again.  After
  *                 an error gqa_device_status re-zeroes it.  Calls that share a
@@ -205,6 +205,9 @@ GQA_API int gqa_device_status(void* workspace, size_t workspace_bytes, void* str
  * until the process exits.
  */
 #define GQA_STATIC_SCRATCH_BYTES (8u * 1024u * 1024u)
+
+/* The part of a workspace that has to be zero before its first use. */
+#define GQA_WORKSPACE_HEAD_BYTES 65792
 
 /*
  * gqa_forward_decode_noalloc -- gqa_forward for the decode path without a

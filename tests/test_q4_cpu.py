@@ -282,3 +282,13 @@ def test_the_way_follows_measured_times(gqa, B, Hkv, g, Sq, Sk, D, way, times):
     p = _problem(gqa, B, Hkv * g, Hkv, Sq, Sk, D, causal=True)
     p.causal_offset = Sk - Sq
     assert gqa.KERNEL_NAMES[_rc(gqa, p)[1].kernel] == way
+
+
+def test_workspace_head(gqa):
+    """What a captured call clears is what the header says has to be zero."""
+    import os
+    import re
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                          "gqa.h")
+    said = re.search(r"#define GQA_WORKSPACE_HEAD_BYTES (\d+)", open(header).read())
+    assert gqa.WORKSPACE_HEAD_BYTES == int(said.group(1))
