@@ -162,10 +162,10 @@ double chunk_ns(const gqa_problem& p, const ChunkShape& s, int sms) {
 // two-tile prefill over 16-bit scratch: the least of the estimated times.  Over
 // 468 problems (1024 to 16384 keys, 2 to 128 kv heads, 4 and 8 query heads
 // each, 3 to 1024 queries, head dims 64 and 128), each timed with every way, it
-// takes 0.4% longer than the fastest in the mean and 12% at most.
+// takes 0.5% longer than the fastest in the mean (10 of them 10% or more).
 //
 // A bf16 slice, in which keys, values and weights are rounded to bf16, has to
-// save a tenth against the tiles, which keep fp16's bits of them.
+// save an eighth against the tiles, which keep fp16's bits of them.
 //
 // With per-sequence lengths a slice takes as long as its longest sequence, the
 // other two as all of them together: counted as three quarters of the most.
@@ -187,7 +187,7 @@ int pick_way(const gqa_problem& p, const DecodeShape& d, int sms, ChunkShape* c,
     best = held * chunk_ns(p, *c, sms);
     way = GQA_KERNEL_Q4_CHUNK;
   }
-  const double bits = way == GQA_KERNEL_Q4_CHUNK && p.dtype == GQA_DTYPE_BF16 ? 1.1 : 1.0;
+  const double bits = way == GQA_KERNEL_Q4_CHUNK && p.dtype == GQA_DTYPE_BF16 ? 1.15 : 1.0;
   return bits * s->ns < best ? GQA_KERNEL_Q4_PREFILL : way;
 }
 

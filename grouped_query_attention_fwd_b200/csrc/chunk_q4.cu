@@ -41,11 +41,11 @@
 // costs the others a barrier and a flag.  An fp16 cache's values are rounded to
 // fp16: 0.0005 against 0.0002.
 //
-// Measured (2 entries, 32/8 heads of 128, 512 queries over 8192 keys): 186 us,
-// 735 TFLOP/s; with more keys a 128-key tile costs an SM 2.4 us with two query
-// tiles and 1.8 us with one (fp16 caches 2.3 and 1.6 us), of which the products
-// need 1.1 us and 0.55 us.  Bound: the unpacking warps and the softmax, which
-// share the issue slots.  With four unpacking warps of twice the work each it
+// Measured (8 entries of 32768 keys, 64/8 heads of 128, 32 queries, bf16): 305
+// us, 900 TFLOP/s; a 128-key tile costs an SM 2.4 us with two query tiles and 1.8
+// us with one (fp16 caches 2.3 and 1.6 us), of which the products need 1.1 us and
+// 0.55 us.  Bound: the unpacking warps and the softmax, which share the issue
+// slots.  With four unpacking warps of twice the work each it
 // took a tenth longer (a tenth less without their arithmetic and stores, a
 // sixth less without the softmax).  A whole S row per thread costs some spills
 // at 168 registers; fewer cost more (152: 5% longer, 136: 38%).
