@@ -47,14 +47,16 @@
 //
 // Reads 160 bytes per key of 128 dims against 512 in 16 bits.  Bound: issue
 // slots of the unpacking and the softmax, then HBM: 16 entries of 32768 keys,
-// 64/8 heads, take 145 us, 4.6 TB/s (103 us at the copy rate); 4096 keys, 32/8
-// heads 23 us, half of it the ranges' ends.  A stage is held until its words
-// are used (handing it back once loaded took 138 us, but a load that has only
-// been issued is no proof that it has come).  Work is cut into ranges of
-// 128-key units as in the 16-bit decode; a producer warp streams K and V
-// records with TMA into a ring, W consumer warps take 32-key chunks in turn, and each keeps a softmax state of its own until the group
-// ends.  80-byte (48-byte) rows make every ldmatrix and parameter read free of
-// bank conflicts without a swizzle.
+// 64/8 heads, take 147 us, 4.6 TB/s (103 us at the copy rate); 4096 keys, 32/8
+// heads 24 us, half of it the ranges' ends.  At head dim 128 a thread wants a few
+// more than its 168 registers: 100 to 210 bytes are spilled.  A stage is held
+// until its words are used and fenced (handing it back once loaded took a twentieth
+// less, but a load that has only been issued is no proof that it has come).  Work
+// is cut into ranges of 128-key units as in the 16-bit decode; a producer warp
+// streams K and V records with TMA into a ring, W consumer warps take 32-key
+// chunks in turn, and each keeps a softmax state of its own until the group ends.
+// 80-byte (48-byte) rows make every ldmatrix and parameter read free of bank
+// conflicts without a swizzle.
 #include <cuda_runtime.h>
 
 #include "decode_sched.cuh"

@@ -312,7 +312,8 @@ GQA_API int gqa_kv_append(const gqa_kv_append_desc* d, void* cache_k, void* cach
  *   code = min(15, rint((x - minimum) / scale)), 0 where scale is 0
  * and read as scale * code + minimum.  The minimum is exact, and a value is
  * off by at most half a step (a step at the top end, where round16 shortened
- * the scale).  A group with a NaN or an infinity, or whose max - min overflows
+ * the scale); where the scale was rounded up, the top of a group that reaches the
+ * type's largest number reads back as an infinity.  A group with a NaN or an infinity, or whose max - min overflows
  * fp32, gets scale = minimum = NaN and reads back NaN throughout.
  *
  * Caches: k and v are uint8 [batch, heads_kv, capacity, record] or, with a

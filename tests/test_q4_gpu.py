@@ -681,3 +681,24 @@ def test_groups_of_different_sizes(gqa, dtype, ratio, D, pattern, Sq):
     bound = bound.reshape(B, H * g, Sq, D) + 1.01 * u.UNIT[dtype] * np.abs(ref) + 2.0 ** -25
     err = np.abs(out - ref)
     assert np.all(err <= bound), float((err / bound).max())
+
+
+def test_a_group_up_to_the_largest_number(gqa):
+    """Spread over fp16's whole range: the scale is rounded up, and the code of
+    the largest number stands for one past it.  Attention does not round it."""
+    x = np.zeros((1, 1, 2, 32), np.float32)
+    x[0, 0, :, 3], x[0, 0, :, 4] = 65504, 30000
+    bits = u.bits_of(x, "fp16")
+    rec = u.quantise(bits, "fp16")
+    want = u.dequantise(rec, 32, "fp16")
+    assert want[0, 0, 0, 3] == 65520.0
+    c = torch.from_numpy(rec).cuda()
+    k, _ = gqa.kv_read_q4(c, c, 32, torch.float16)
+    got = u.to64(k)
+    assert np.all(np.isposinf(got[..., 3])) and np.all(np.isfinite(got[..., :3]))
+    q = torch.zeros(1, 1, 1, 32, dtype=torch.float16, device="cuda")
+    zero = torch.from_numpy(u.quantise(np.zeros_like(bits), "fp16")).cuda()
+    both = torch.cat([c[:, :, :1], zero[:, :, :1]], 2)
+    out = u.to64(gqa.forward_q4(q, both, both))  # the mean of the two keys
+    _ok(gqa)
+    assert abs(out[0, 0, 0, 3] - 32760.0) <= 2.0 ** -11 * 32760 * 2
