@@ -426,3 +426,37 @@ def test_weight_on_a_key_of_zeros(gqa, dtype, share):
             2.0 ** -32 * vv.abs().sum(0) + 1.01 * u.UNIT[dtype] * ref.abs() + 2.0 ** -25
         err = (out[0, h] - fit * ref).abs()
         assert torch.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("Sq,Sk", [(512, 2048), (20, 20000)])
+def test_one_record_past_fp16(gqa, Sq, Sk):
+    """A single value row that fp16 does not hold: the CTAs that meet it go over
+    to bf16, and their partials meet those of the others."""
+    q, (ck, cv), kw, _, _ = _chunk_case(gqa, 128, Sq, Sk, 1.0, 1.0, 1.0, 44)
+    B, Hq, D, at = 2, 8, 128, Sk // 3
+    row = torch.zeros(1, 2, 1, D, device="cuda")
+    row[:, 1] = torch.linspace(-3e5, 3e5, D, device="cuda")
+    lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+    keep = cv[0, 0, at].clone()
+    gqa.kv_append_q4(cv[:1].clone(), cv[:1], row.bfloat16(), row.bfloat16(), lens)
+    cv[0, 0, at] = keep  # (head 0 stays as it was)
+    vals = []
+    for c in (ck, cv):
+        par = c[..., :16].contiguous().view(torch.bfloat16).double().unflatten(-1, (4, 2))
+        code = torch.stack([c[..., 16:] % 16, c[..., 16:] // 16], -1).double().flatten(-2)
+        vals.append((code.unflatten(-1, (4, 32)) * par[..., :1] + par[..., 1:]).flatten(-2))
+    out = gqa.forward_q4(q, ck, cv, **kw).double()
+    assert gqa.device_status() == gqa.GQA_OK
+    see = torch.arange(Sk, device="cuda") <= torch.arange(Sq, device="cuda")[:, None] + Sk - Sq
+    for b in range(B):
+        for h in range(Hq):
+            k, v, qh = vals[0][b, h // 4], vals[1][b, h // 4], q[b, h].double()
+            p = torch.softmax((qh @ k.T * kw["scale"]).masked_fill(~see, -math.inf), -1)
+            ref = p @ v
+            # bf16's roundings of keys, values and weights where the row is.
+            unit = 2.0 ** -8 if b == 0 else 2.0 ** -11
+            move = kw["scale"] * (qh.abs() @ k.abs().T).amax(-1, keepdim=True)
+            bound = (p @ v.abs()) * (2.02 * unit + 2.1 * unit * move + 2.0 ** -14) + \
+                1.01 * 2.0 ** -8 * ref.abs()
+            err = (out[b, h] - ref).abs()
+            assert torch.all(err <= bound), (b, h, float((err / bound).max()))
