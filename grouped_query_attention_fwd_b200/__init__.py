@@ -181,7 +181,7 @@ def _torch():
 
 
 _workspaces = {}
-_captured_workspaces = {}  # those that a graph capture was given, by address: a graph points at them
+_captured_workspaces = {}  # by address: those that a capture was given, graphs point at them
 
 
 def _dtype_code(t) -> int:

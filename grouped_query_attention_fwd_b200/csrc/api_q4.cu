@@ -139,7 +139,8 @@ SlicePlan plan_slices(const gqa_problem& p, int sms) {
   const double bytes = 2.0 * double(p.batch * p.heads_kv) *
                        double(keys * (q4::record_bytes(static_cast<int>(p.head_dim)) +
                                          2 * p.head_dim));
-  s.ns = double(s.slices) * (kSliceNs + rounds * double((keys + 127) / 128) * two_tile_ns(p.head_dim)) +
+  const double tiles = rounds * double((keys + 127) / 128);
+  s.ns = double(s.slices) * (kSliceNs + tiles * two_tile_ns(p.head_dim)) +
          bytes / kReadBytesPerNs;
   return s;
 }

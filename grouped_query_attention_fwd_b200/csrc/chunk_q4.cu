@@ -809,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                 tmem_st16(o_col + X * 128 + c * 32, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-                tmem_st16(o_col + X * 128 + c * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+                tmem_st16(o_col + X * 128 + c * 32 + 16,
+                          *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
               }
             }
             begun = true;
@@ -822,8 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Epilogue: out, or this CTA's partial of a split group.
         const bool some = me.nt_end > me.nt_beg;
         const bool split = me.c_lo != me.c_hi;
-        ok = __all_sync(0xffffffffu, ok && (!some || mbar_wait_hot(o_final, n_share & 1u, abort_flag,
-                                                                   a.err, kErrPrefillWait)));
+        ok = __all_sync(0xffffffffu,
+                        ok && (!some || mbar_wait_hot(o_final, n_share & 1u, abort_flag, a.err,
+                                                      kErrPrefillWait)));
         // Weights of O_0 and O_1 in this row's result.
         float w0 = X == 0 ? 1.f : 0.f, w1 = X == 0 ? 0.f : 1.f;
         if (nq == 1 && live) {
@@ -893,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     make_float4(o[d + kAt[e]], o[d + kAt[e + 1]], o[d + kAt[e + 2]],
                                 o[d + kAt[e + 3]]);
           } else {
-            uint16_t* orow = a.out + pr.b * a.os[0] + static_cast<int64_t>(pr.kv * a.g + hh) * a.os[1] +
+            uint16_t* orow = a.out + pr.b * a.os[0] +
+                             static_cast<int64_t>(pr.kv * a.g + hh) * a.os[1] +
                              static_cast<int64_t>(q) * a.os[2] + c * 32;
 #pragma unroll
             for (int d = 0; d < 32; d += 8) {

@@ -930,7 +930,8 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
             // The reference goes to the maximum, rounded up; l and corr follow by
             // alpha (0 for a row without a key so far).  Powers of two are kept as
             // the bits of their exponent.
-            const bool begun = __any_sync(0xffffffffu, m_ref[0] > -INFINITY || m_ref[1] > -INFINITY);
+            const bool begun =
+                __any_sync(0xffffffffu, m_ref[0] > -INFINITY || m_ref[1] > -INFINITY);
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -993,7 +994,8 @@ __global__ void __launch_bounds__(Q4Layout<NG>::kThreads, 1)
                             : 0.f;
                 if (m_ref[e] > -INFINITY) high = max(high, to[e]);
               }
-              const uint32_t code = type_power<F16>(kLazyScaleLog2 + 127 - static_cast<int>(high >> 23));
+              const uint32_t code =
+                  type_power<F16>(kLazyScaleLog2 + 127 - static_cast<int>(high >> 23));
               limit[t / 2] = t % 2 == 0 ? code : limit[t / 2] | (code << 16);
               pow[t] = f2_pack(__uint_as_float(to[0]), __uint_as_float(to[1]));
               if (begun) {

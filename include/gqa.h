@@ -174,9 +174,10 @@ GQA_API int gqa_query(const gqa_problem* p, int sm_count, gqa_plan* plan);
  *   mask:         device uint8 pointer if p->has_mask, else ignored (may be NULL).
  *   workspace:    device scratch of at least plan.workspace_bytes, 256-byte
  *                 aligned, owned by the caller, ZERO-FILLED before its first
- *                 use.  Its head (GQA_WORKSPACE_HEAD_BYTES) holds the error word
- *                 and, from byte 256 on, the decode ticket counters; every call leaves that
- *                 head as it found it, so one workspace serves any sequence
+ *                 use.  Its head (GQA_WORKSPACE_HEAD_BYTES) holds the error
+ *                 word and, from byte 256 on, the decode ticket counters;
+ *                 every call leaves that head as it found it, so one
+ *                 workspace serves any sequence
  *                 of calls of any shapes without being cleared again.  After
  *                 an error gqa_device_status re-zeroes it.  Calls that share a
  *                 workspace must be ordered on one stream; calls that overlap
@@ -312,9 +313,10 @@ GQA_API int gqa_kv_append(const gqa_kv_append_desc* d, void* cache_k, void* cach
  *   code = min(15, rint((x - minimum) / scale)), 0 where scale is 0
  * and read as scale * code + minimum.  The minimum is exact, and a value is
  * off by at most half a step (a step at the top end, where round16 shortened
- * the scale); where the scale was rounded up, the top of a group that reaches the
- * type's largest number reads back as an infinity.  A group with a NaN or an infinity, or whose max - min overflows
- * fp32, gets scale = minimum = NaN and reads back NaN throughout.
+ * the scale); where the scale was rounded up, the top of a group that reaches
+ * the type's largest number reads back as an infinity.  A group with a NaN or
+ * an infinity, or whose max - min overflows fp32, gets scale = minimum = NaN
+ * and reads back NaN throughout.
  *
  * Caches: k and v are uint8 [batch, heads_kv, capacity, record] or, with a
  * block table, pools [num_pages, heads_kv, page_size, record].  Their strides
@@ -385,8 +387,9 @@ GQA_API int gqa_kv_read_q4(const gqa_kv_q4_desc* d, const void* cache_k, const v
  * once to 16 bits, on the way to the tensor cores (GQA_KERNEL_Q4_CHUNK: to fp16,
  * or to bf16 where a bf16 cache's values or queries are past what fp16 holds) or
  * in scratch (GQA_KERNEL_Q4_PREFILL: to the cache's type; part of
- * plan.workspace_bytes, at most 1 GiB unless one head's keys alone need more).  What decides is the estimated time
- * of each; a single token always takes the first.
+ * plan.workspace_bytes, at most 1 GiB unless one head's keys alone need more).
+ * What decides is the estimated time of each; a single token always takes the
+ * first.
  * A key that no query of the block can see by lengths, diagonal and window
  * never reaches the result, whatever its record holds.  One that some query
  * sees, or that only the mask hides, stays out of the other rows with
@@ -419,7 +422,8 @@ GQA_API int gqa_debug_decode_trace(void* device_buffer, int64_t bytes);
  * gqa_debug_decode_withhold -- test of the kernels' bounded waits (failure
  * detection without a GPU fault; the pages have no counterpart).  The NEXT
  * decode launch of the process (gqa_forward, gqa_forward_decode_noalloc, or
- * gqa_forward_q4 with GQA_KERNEL_Q4) uses `wait_limit_ns` (1000 .. 1e9) as the limit of every internal wait and,
+ * gqa_forward_q4 with GQA_KERNEL_Q4) uses `wait_limit_ns` (1000 .. 1e9) as the
+ * limit of every internal wait and,
  * if `unit` >= 0, its producer never issues the copies of that 128-key unit
  * (index in launch order) and issues nothing after it: the consumers' wait
  * for the unit runs out, the CTA unwinds (every copy already issued lands

@@ -284,7 +284,8 @@ def test_scales_and_blocks_without_a_diagonal(gqa, Sq, masked, causal, dtype, ke
     for b, n in enumerate(lens.tolist()):
         see = torch.ones(Sq, n, dtype=torch.bool, device="cuda")
         if causal:
-            see = torch.arange(n, device="cuda") <= torch.arange(Sq, device="cuda")[:, None] + n - Sq
+            top = torch.arange(Sq, device="cuda")[:, None] + n - Sq
+            see = torch.arange(n, device="cuda") <= top
         if masked:
             see = see & kw["mask"][b, :, :n]
         for h in range(Hq):
@@ -318,7 +319,8 @@ def _chunk_case(gqa, D, Sq, Sk, kf, vf, qf, seed, dtype="bf16", groups=None):
         par = c[..., :4 * G].contiguous().view(u.TORCH[dtype]).double().unflatten(-1, (G, 2))
         code = torch.stack([c[..., 16:] % 16, c[..., 16:] // 16], -1).double().flatten(-2)
         caches.append(c)
-        values.append((code.unflatten(-1, (G, 32)) * par[..., :1] + par[..., 1:]).flatten(-2)[..., :D])
+        x = code.unflatten(-1, (G, 32)) * par[..., :1] + par[..., 1:]
+        values.append(x.flatten(-2)[..., :D])
     q = (torch.randn(B, Hq, Sq, D, generator=gen, device="cuda") * qf).to(u.TORCH[dtype])
     kw = dict(causal=True, causal_offset="bottom_right", scale=1.0 / (kf * qf * math.sqrt(D)))
     assert gqa.query_q4(q, *caches, **kw)["kernel_name"] == "q4_chunk"
@@ -370,8 +372,8 @@ def test_bf16_chunks_of_any_size(gqa, kf, vf, qf, groups, D, Sq, Sk):
     ws = torch.zeros(plan["workspace_bytes"], dtype=torch.uint8, device="cuda")
     for _ in range(2):
         out = gqa.forward_q4(q, *caches, workspace=ws, **kw).double()
-        err = (out - ref).abs()
-        assert torch.all(err <= bound(2.0 ** -8, 2.0 ** -8)), float((err / bound(2.0 ** -8, 2.0 ** -8)).max())
+        off = (out - ref).abs() / bound(2.0 ** -8, 2.0 ** -8)
+        assert torch.all(off <= 1.0), float(off.max())
         assert not ws[:256].any()
         out = gqa.forward_q4(nq, *nc, workspace=ws, **nkw).double()
         assert torch.all((out - nref).abs() <= nbound(2.0 ** -11, 2.0 ** -8))
